@@ -9,6 +9,7 @@ stream handle (int) or a ``torch.cuda.Stream``.
     Y = S(X) W^T + X (L_A L_B)^T        mode = MODE_SPARSE
     Y = X W^T                           mode = MODE_DENSE_SKIP
     H = GELU(up(X)), Y = down(H)        rtlynx_mlp_block (two such layers)
+    R(p) x,  R(p) (w x / rms(x))        rtlynx_rope, rtlynx_qk_norm_rope (query and key heads)
 
 (RT-Lynx summary page, four-step pipeline paragraph, steps 1-3.)
 
@@ -33,6 +34,11 @@ ERR_CUDA = 3
 ERR_OOM = 4
 ERR_DEVICE_TIMEOUT = 5
 
+BF16, FP16, FP32 = 0, 1, 2                    # rtlynx_dtype
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1            # rtlynx_rope_pairing
+POS_INT32, POS_INT64, POS_FP32 = 0, 1, 2      # rtlynx_pos_type
+MAX_AXES = 4
+
 # Every symbol include/rtlynx.h declares.
 ABI_SYMBOLS = (
     "rtlynx_linear", "rtlynx_workspace_size", "rtlynx_linear_ws", "rtlynx_linear_ws_events",
@@ -40,6 +46,8 @@ ABI_SYMBOLS = (
     "rtlynx_sparsify_debug", "rtlynx_linear_host", "rtlynx_mlp_block", "rtlynx_linear_noalloc",
     "rtlynx_kernel_launches", "rtlynx_schedule_info",
     "rtlynx_quantize_weight_fp8", "rtlynx_linear_fp8", "rtlynx_linear_fp8_events", "rtlynx_sparsify_fp8_debug",
+    "rtlynx_rope", "rtlynx_rope_backward", "rtlynx_qk_norm_rope", "rtlynx_qk_norm_rope_workspace_size",
+    "rtlynx_qk_norm_rope_backward",
     "rtlynx_wait_selftest", "rtlynx_stream_status", "rtlynx_status_string", "rtlynx_release",
 )
 
@@ -65,6 +73,17 @@ class Schedule(ctypes.Structure):
         "prologue_ctas", "prologue_tiles", "prologue_max_segs", "row_blocks", "k_tiles_per_block",
         "gemm_pairs", "gemm_tiles", "tail_full", "tail_split", "tail_units", "k_stages", "lora_stages",
         "small_path")]
+
+
+class HeadsView(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("heads", ctypes.c_int64), ("stride_b", ctypes.c_int64),
+                ("stride_s", ctypes.c_int64), ("stride_h", ctypes.c_int64)]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("axis_dim", ctypes.c_int32 * MAX_AXES), ("pairing", ctypes.c_int32),
+                ("pos_type", ctypes.c_int32), ("theta", ctypes.c_double),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double))]
 
 
 def lib() -> ctypes.CDLL:
@@ -107,6 +126,18 @@ def lib() -> ctypes.CDLL:
         L.rtlynx_kernel_launches.restype = i
         L.rtlynx_schedule_info.argtypes = [i64, i64, i64, i64, i, ctypes.POINTER(Schedule)]
         L.rtlynx_schedule_info.restype = i
+        hv, spec, f = ctypes.POINTER(HeadsView), ctypes.POINTER(RopeSpec), ctypes.c_float
+        L.rtlynx_rope.argtypes = [hv, hv, hv, hv, i64, i64, i64, i, spec, p, i64, i64, i64, p]
+        L.rtlynx_rope.restype = i
+        L.rtlynx_rope_backward.argtypes = L.rtlynx_rope.argtypes
+        L.rtlynx_rope_backward.restype = i
+        L.rtlynx_qk_norm_rope.argtypes = [hv, hv, p, p, hv, hv, i64, i64, i64, i, f, spec, p, i64, i64, i64, p]
+        L.rtlynx_qk_norm_rope.restype = i
+        L.rtlynx_qk_norm_rope_workspace_size.argtypes = [i64]
+        L.rtlynx_qk_norm_rope_workspace_size.restype = ctypes.c_size_t
+        L.rtlynx_qk_norm_rope_backward.argtypes = [hv, hv, hv, hv, p, p, hv, hv, p, p, i64, i64, i64, i, f, spec, p,
+                                                   i64, i64, i64, p, ctypes.c_size_t, p]
+        L.rtlynx_qk_norm_rope_backward.restype = i
         L.rtlynx_wait_selftest.argtypes = [i64, p]
         L.rtlynx_wait_selftest.restype = i
         L.rtlynx_stream_status.argtypes = [p]
@@ -234,6 +265,36 @@ def rtlynx_sparsify_fp8_debug(X, M, D_in, codes, meta, qx, stream=None) -> int:
                                                   _stream(stream)), "rtlynx_sparsify_fp8_debug")
 
 
+def rtlynx_rope(q, k, q_out, k_out, B, S, D_head, dtype, spec, positions, pos_strides, stream=None) -> int:
+    """q, k, q_out, k_out: HeadsView (k and k_out may be None); spec: RopeSpec; pos_strides: (batch, token, axis)."""
+    return _check(lib().rtlynx_rope(q, k, q_out, k_out, B, S, D_head, dtype, spec, _ptr(positions), *pos_strides,
+                                    _stream(stream)), "rtlynx_rope")
+
+
+def rtlynx_rope_backward(dq_out, dk_out, dq, dk, B, S, D_head, dtype, spec, positions, pos_strides,
+                         stream=None) -> int:
+    return _check(lib().rtlynx_rope_backward(dq_out, dk_out, dq, dk, B, S, D_head, dtype, spec, _ptr(positions),
+                                             *pos_strides, _stream(stream)), "rtlynx_rope_backward")
+
+
+def rtlynx_qk_norm_rope(q, k, w_q, w_k, q_out, k_out, B, S, D_head, dtype, eps, spec, positions, pos_strides,
+                        stream=None) -> int:
+    return _check(lib().rtlynx_qk_norm_rope(q, k, _ptr(w_q), _ptr(w_k), q_out, k_out, B, S, D_head, dtype, eps, spec,
+                                            _ptr(positions), *pos_strides, _stream(stream)), "rtlynx_qk_norm_rope")
+
+
+def rtlynx_qk_norm_rope_workspace_size(D_head) -> int:
+    return int(lib().rtlynx_qk_norm_rope_workspace_size(D_head))
+
+
+def rtlynx_qk_norm_rope_backward(dq_out, dk_out, q, k, w_q, w_k, dq, dk, dw_q, dw_k, B, S, D_head, dtype, eps, spec,
+                                 positions, pos_strides, workspace, ws_bytes, stream=None) -> int:
+    return _check(lib().rtlynx_qk_norm_rope_backward(dq_out, dk_out, q, k, _ptr(w_q), _ptr(w_k), dq, dk, _ptr(dw_q),
+                                                     _ptr(dw_k), B, S, D_head, dtype, eps, spec, _ptr(positions),
+                                                     *pos_strides, _ptr(workspace), ws_bytes, _stream(stream)),
+                  "rtlynx_qk_norm_rope_backward")
+
+
 def rtlynx_kernel_launches(M, D_in, D_out, R, mode) -> int:
     return int(lib().rtlynx_kernel_launches(M, D_in, D_out, R, mode))
 
@@ -277,3 +338,196 @@ def linear(X, W, L_A=None, L_B=None, mode: int = MODE_SPARSE, out=None, stream=N
     Y = out if out is not None else torch.empty((M, D_out), dtype=torch.bfloat16, device=X.device)
     rtlynx_linear(X, W, L_A if R else None, L_B if R else None, Y, M, D_in, D_out, R, mode, stream)
     return Y
+
+
+class _Launch:
+    """Where a torch-level call runs: the tensors' device, and the stream whose
+    allocator pool its outputs and workspace come from (`stream`, or the
+    device's current one), so that memory is never handed on while in use."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.device, self.ctx = device, None
+        if stream is None:
+            self.handle = int(torch.cuda.current_stream(device).cuda_stream)
+            if torch.cuda.current_device() != device.index:
+                self.ctx = torch.cuda.device(device)
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            elif stream.device != device:
+                raise ValueError(f"stream of {stream.device}, tensors on {device}")
+            self.handle = int(stream.cuda_stream)
+            self.ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            return self.ctx.__exit__(*exc)
+
+
+class Rope:
+    """A rotation by position, to keep and pass to rope() and qk_norm_rope().
+
+    axes      channels of each axis, e.g. (44, 42, 42) for time, height and width of a head of 128, (128,) for text;
+              channels past their sum pass through
+    theta     base of the frequencies theta^(-2 j / axis)
+    pairing   ROPE_INTERLEAVED (channels 2 i, 2 i + 1) or ROPE_HALF (channels i, i + sum(axes) / 2)
+    inv_freq  the frequencies themselves, sum(axes) / 2 numbers in pair order, instead of theta
+    """
+
+    def __init__(self, axes, theta=10000.0, pairing=ROPE_INTERLEAVED, inv_freq=None):
+        self.axes = tuple(int(a) for a in axes)
+        if not 1 <= len(self.axes) <= MAX_AXES:
+            raise ValueError(f"one to {MAX_AXES} axes, got {len(self.axes)}")
+        if any(a < 2 or a % 2 for a in self.axes):
+            raise ValueError(f"every axis has an even number of channels, got {self.axes}")
+        self._freq = None
+        if inv_freq is not None:
+            values = [float(v) for v in inv_freq]
+            if len(values) != sum(self.axes) // 2:
+                raise ValueError(f"inv_freq has {len(values)} values, the axes {sum(self.axes) // 2} pairs")
+            self._freq = (ctypes.c_double * len(values))(*values)
+        dims = (ctypes.c_int32 * MAX_AXES)(*self.axes)
+        freq = ctypes.cast(self._freq, ctypes.POINTER(ctypes.c_double)) if self._freq is not None else None
+        self.specs = tuple(RopeSpec(len(self.axes), dims, int(pairing), t, float(theta), freq)
+                           for t in (POS_INT32, POS_INT64, POS_FP32))
+
+
+def _dtype_code(dtype):
+    import torch
+    code = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}.get(dtype)
+    if code is None:
+        raise ValueError(f"bf16, fp16 or fp32 tensors, got {dtype}")
+    return code
+
+
+def _heads_view(t, like=None, what="heads"):
+    """HeadsView of t [S, H, D] or [B, S, H, D] (any strides, channels contiguous)."""
+    if not t.is_cuda or t.dim() not in (3, 4) or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what}: CUDA tensor [S, H, D] or [B, S, H, D] with contiguous channels")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{what}: {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
+    st = t.stride()
+    return HeadsView(t.data_ptr(), t.shape[-2], st[0] if t.dim() == 4 else 0, st[-3], st[-2])
+
+
+def _heads_out(out, like, what):
+    import torch
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if out.shape != like.shape:
+        raise ValueError(f"{what}: shape {tuple(out.shape)}, expected {tuple(like.shape)}")
+    return out
+
+
+def _heads_sizes(q, k):
+    B = q.shape[0] if q.dim() == 4 else 1
+    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]):
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} differ in more than their heads")
+    return B, q.shape[-3], q.shape[-1]
+
+
+def _rope_positions(positions, rope, q, B, S):
+    """(spec, positions, strides) for positions [S, axes] or [B, S, axes]."""
+    import torch
+    kind = {torch.int32: POS_INT32, torch.int64: POS_INT64, torch.float32: POS_FP32}.get(positions.dtype)
+    if kind is None or positions.device != q.device:
+        raise ValueError(f"positions: int32, int64 or float32 on {q.device}, got {positions.dtype} on "
+                         f"{positions.device}")
+    shape, st = tuple(positions.shape), positions.stride()
+    if shape == (S, len(rope.axes)):
+        strides = (0, st[0], st[1])
+    elif shape == (B, S, len(rope.axes)):
+        strides = st
+    else:
+        raise ValueError(f"positions {shape}, expected {(S, len(rope.axes))} or {(B, S, len(rope.axes))}")
+    return rope.specs[kind], strides
+
+
+def _norm_weight(w, q, what):
+    if w is not None and (tuple(w.shape) != (q.shape[-1],) or w.dtype != q.dtype or w.device != q.device or
+                          not w.is_contiguous()):
+        raise ValueError(f"{what}: contiguous [{q.shape[-1]}] {q.dtype} on {q.device}")
+    return w
+
+
+def _run_rope(q, k, positions, rope, out, stream, backward):
+    qv = _heads_view(q, what="q")
+    kv = None if k is None else _heads_view(k, q, "k")
+    code = _dtype_code(q.dtype)
+    B, S, D = _heads_sizes(q, k)
+    spec, strides = _rope_positions(positions, rope, q, B, S)
+    with _Launch(q.device, stream) as handle:
+        q_out = _heads_out(out[0] if out else None, q, "q_out")
+        k_out = None if k is None else _heads_out(out[1] if out else None, k, "k_out")
+        call = rtlynx_rope_backward if backward else rtlynx_rope
+        call(qv, kv, _heads_view(q_out, q, "q_out"), None if k is None else _heads_view(k_out, q, "k_out"), B, S, D,
+             code, spec, positions, strides, handle)
+    return q_out, k_out
+
+
+def rope(q, k, positions, rope, out=None, stream=None):
+    """(R q, R k) for q [B, S, Hq, D] and k [B, S, Hk, D] (or [S, H, D], or k None), any strides.
+
+    positions [S, axes] or [B, S, axes] (int32, int64, float32), rope a Rope; out=(q, k) works in place."""
+    return _run_rope(q, k, positions, rope, out, stream, False)
+
+
+def rope_backward(dq_out, dk_out, positions, rope, out=None, stream=None):
+    """Gradients of rope()'s inputs from those of its outputs; out=(dq_out, dk_out) works in place."""
+    return _run_rope(dq_out, dk_out, positions, rope, out, stream, True)
+
+
+def qk_norm_rope(q, k, w_q, w_k, positions, rope, eps=1e-6, out=None, stream=None):
+    """rope() of the heads' RMS norms: (R (w_q q / rms q), R (w_k k / rms k)); w_q, w_k [D] in q's type, or None."""
+    qv = _heads_view(q, what="q")
+    kv = None if k is None else _heads_view(k, q, "k")
+    code = _dtype_code(q.dtype)
+    B, S, D = _heads_sizes(q, k)
+    spec, strides = _rope_positions(positions, rope, q, B, S)
+    _norm_weight(w_q, q, "w_q")
+    _norm_weight(w_k, q, "w_k")
+    with _Launch(q.device, stream) as handle:
+        q_out = _heads_out(out[0] if out else None, q, "q_out")
+        k_out = None if k is None else _heads_out(out[1] if out else None, k, "k_out")
+        rtlynx_qk_norm_rope(qv, kv, w_q, w_k, _heads_view(q_out, q, "q_out"),
+                            None if k is None else _heads_view(k_out, q, "k_out"), B, S, D, code, eps, spec,
+                            positions, strides, handle)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, w_q, w_k, positions, rope, eps=1e-6, out=None, weight_grads=True,
+                          stream=None):
+    """(dq, dk, dw_q, dw_k) of qk_norm_rope(); dw_q, dw_k are float32 [D], None without weight_grads or a weight."""
+    import torch
+    qv, gqv = _heads_view(q, what="q"), _heads_view(dq_out, q, "dq_out")
+    kv = None if k is None else _heads_view(k, q, "k")
+    if (dk_out is None) != (k is None) or dq_out.shape != q.shape or (k is not None and dk_out.shape != k.shape):
+        raise ValueError("dq_out and dk_out have the shapes of q and k")
+    gkv = None if k is None else _heads_view(dk_out, q, "dk_out")
+    code = _dtype_code(q.dtype)
+    B, S, D = _heads_sizes(q, k)
+    spec, strides = _rope_positions(positions, rope, q, B, S)
+    _norm_weight(w_q, q, "w_q")
+    _norm_weight(w_k, q, "w_k")
+    with _Launch(q.device, stream) as handle:
+        dq = _heads_out(out[0] if out else None, q, "dq")
+        dk = None if k is None else _heads_out(out[1] if out else None, k, "dk")
+        dw_q = dw_k = ws = None
+        if weight_grads and w_q is not None:
+            dw_q = torch.empty(D, dtype=torch.float32, device=q.device)
+        if weight_grads and w_k is not None and k is not None:
+            dw_k = torch.empty(D, dtype=torch.float32, device=q.device)
+        ws_bytes = 0
+        if dw_q is not None or dw_k is not None:
+            ws_bytes = rtlynx_qk_norm_rope_workspace_size(D)
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        rtlynx_qk_norm_rope_backward(gqv, gkv, qv, kv, w_q, w_k, _heads_view(dq, q, "dq"),
+                                     None if k is None else _heads_view(dk, q, "dk"), dw_q, dw_k, B, S, D, code, eps,
+                                     spec, positions, strides, ws, ws_bytes, handle)
+    return dq, dk, dw_q, dw_k

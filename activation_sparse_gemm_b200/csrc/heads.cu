@@ -1,0 +1,698 @@
+// Query and key heads between the qkv layer and attention: rotary positions
+// with several axes, RMS norm of each head fused with the rotation, and the
+// gradients of both.
+//
+//   n = x r,  r = (mean_c x_c^2 + eps)^(-1/2)     (norm forms only)
+//   y = R(p) (n w)                                 pair i of axis a turned by
+//                                                  p_a f_i radians
+//   backward, g = R(p)^T dy:
+//   dw = sum over tokens and heads of g n
+//   dx = r (g w - n mean_c(g w n))
+//
+// Every element is read once and written once and needs a handful of
+// operations, so memory bounds it.  A warp owns one token of one tensor and
+// walks over that token's heads: a lane keeps the same eight channels of
+// every head, so the cosines, sines and norm weights of its channels are
+// computed or loaded once a token and stay in registers, and no table of
+// angles is read.  Eight channels are 16 bytes of a 16-bit type; a head of d
+// channels takes d / 8 lanes, and several heads share a pass of the warp when
+// d <= 128.  kUnroll passes are loaded before the first is used.
+//
+// Angles: position x frequency / 2 pi in 64 bits, reduced to an eighth of a
+// turn there, so a position of 2^24 loses nothing; sine and cosine of the
+// remainder in 32.  Sums of squares and all other sums are held in 32 bits,
+// outputs rounded once.
+//
+// The weights' gradients: each block sums its tokens in a fixed order into a
+// row of the caller's workspace, and a second kernel adds the rows in order;
+// no atomics, so equal calls give equal bits.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "../../include/rtlynx.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace rtlynx {
+namespace {
+
+constexpr int kHeadThreads = 256;
+constexpr int kHeadWarps = kHeadThreads / 32;
+constexpr int kMaxDim = 256;
+constexpr int kMaxPairs = kMaxDim / 2;
+constexpr int kHeadGradRows = 512;  // rows of partial sums the workspace holds for each tensor
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+
+enum Kind { kRope = 0, kNorm = 1, kNormBackward = 2 };
+
+// One tensor of the call: x is read (the gradient dy too in backward), y written.
+struct HeadTensor {
+    const void* x;
+    const void* dy;
+    void* y;
+    const void* w;
+    float* part;  // backward: [blocks, dim] partial sums of the weight's gradient
+    int64_t xb, xs, xh, gb, gs, gh, yb, ys, yh;  // strides of batch, token, head, in elements
+    uint32_t heads, groups, passes;  // a token's heads are cut into `groups` runs of `passes` warp passes
+    uint32_t items, blocks;
+};
+
+struct HeadArgs {
+    HeadTensor t[2];  // queries, keys
+    const void* positions;
+    int64_t pb, ps, pa;  // strides of the positions: batch, token, axis
+    int pos_type;
+    uint32_t tokens;  // per sequence
+    int dim, pairs;
+    float eps, sin_sign;
+    uint8_t axis[kMaxPairs];
+    double turns[kMaxPairs];  // frequency / 2 pi
+};
+
+template <typename T>
+struct Raw {
+    uint32_t r[2 * sizeof(T)];
+};
+
+__device__ __forceinline__ float2 widen(uint32_t u, __nv_bfloat16) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 widen(uint32_t u, __half) { return __half22float2(*reinterpret_cast<__half2*>(&u)); }
+
+__device__ __forceinline__ uint32_t narrow(float a, float b, __nv_bfloat16) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t narrow(float a, float b, __half) {
+    __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw<T>& raw, float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(raw.r[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = widen(raw.r[j], T());
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void pack(const float (&v)[8], Raw<T>& raw) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) raw.r[j] = __float_as_uint(v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) raw.r[j] = narrow(v[2 * j], v[2 * j + 1], T());
+    }
+}
+
+// A lane's eight channels are two runs of four, at offsets a and b.  They
+// are one run of eight (b = a + 4) unless HALF pairs channel i with channel
+// i + rotated / 2.  Outputs may be the inputs' own memory, so these are plain
+// loads, not the read-only path.
+template <typename T, bool HALF>
+__device__ __forceinline__ void load8(const T* p, int a, int b, Raw<T>& raw) {
+    if constexpr (sizeof(T) == 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p + a), v = *reinterpret_cast<const uint4*>(p + b);
+        raw.r[0] = u.x, raw.r[1] = u.y, raw.r[2] = u.z, raw.r[3] = u.w;
+        raw.r[4] = v.x, raw.r[5] = v.y, raw.r[6] = v.z, raw.r[7] = v.w;
+    } else if constexpr (HALF) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p + a), v = *reinterpret_cast<const uint2*>(p + b);
+        raw.r[0] = u.x, raw.r[1] = u.y, raw.r[2] = v.x, raw.r[3] = v.y;
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(p + a);
+        raw.r[0] = u.x, raw.r[1] = u.y, raw.r[2] = u.z, raw.r[3] = u.w;
+    }
+}
+
+template <typename T, bool HALF>
+__device__ __forceinline__ void store8(T* p, int a, int b, const Raw<T>& raw) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<uint4*>(p + a) = make_uint4(raw.r[0], raw.r[1], raw.r[2], raw.r[3]);
+        *reinterpret_cast<uint4*>(p + b) = make_uint4(raw.r[4], raw.r[5], raw.r[6], raw.r[7]);
+    } else if constexpr (HALF) {
+        *reinterpret_cast<uint2*>(p + a) = make_uint2(raw.r[0], raw.r[1]);
+        *reinterpret_cast<uint2*>(p + b) = make_uint2(raw.r[2], raw.r[3]);
+    } else {
+        *reinterpret_cast<uint4*>(p + a) = make_uint4(raw.r[0], raw.r[1], raw.r[2], raw.r[3]);
+    }
+}
+
+// Turns the lane's four pairs; pairs that are not rotated keep their bits
+// (multiplying by a sine of zero would make NaN of an infinity).
+template <bool HALF>
+__device__ __forceinline__ void rotate(float (&v)[8], const float (&c)[4], const float (&s)[4], uint32_t turned) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int a = HALF ? j : 2 * j, b = HALF ? j + 4 : 2 * j + 1;
+        const float x = v[a], y = v[b];
+        if (turned >> j & 1u) {
+            v[a] = fmaf(x, c[j], -y * s[j]);
+            v[b] = fmaf(x, s[j], y * c[j]);
+        }
+    }
+}
+
+template <int LANES>
+__device__ __forceinline__ float head_sum(float v) {
+#pragma unroll
+    for (int m = LANES / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+    return v;
+}
+
+template <typename T, int LANES, bool HALF, int KIND>
+__global__ void __launch_bounds__(kHeadThreads) rtlynx_heads_kernel(const __grid_constant__ HeadArgs args) {
+    constexpr int kHeadsPerPass = 32 / LANES;
+    constexpr int kUnroll = sizeof(T) == 4 ? 2 : (KIND == kNormBackward ? 2 : 4);
+    __shared__ double turns[kMaxPairs];
+    __shared__ uint8_t axis[kMaxPairs];
+    __shared__ float sums[KIND == kNormBackward ? kHeadWarps * 32 * 8 : 1];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < args.pairs; i += kHeadThreads) {
+        turns[i] = args.turns[i];
+        axis[i] = args.axis[i];
+    }
+    __syncthreads();
+    grid_dependency_wait();
+
+    const bool keys = blockIdx.x >= args.t[0].blocks;
+    const HeadTensor& t = args.t[keys ? 1 : 0];
+    const uint32_t block = blockIdx.x - (keys ? args.t[0].blocks : 0u);
+
+    const int chunk = lane % LANES, sub = lane / LANES;
+    const bool active = chunk * 8 < args.dim;
+    const int rotated = 2 * args.pairs;
+    // channel offsets of the lane's two runs of four
+    int a = 8 * chunk, b = 8 * chunk + 4;
+    if (HALF && 8 * chunk < rotated) {
+        a = 4 * chunk;
+        b = args.pairs + 4 * chunk;
+    }
+
+    float w[8];
+    if constexpr (KIND != kRope) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+        if (active && t.w) {
+            Raw<T> raw;
+            load8<T, HALF>(static_cast<const T*>(t.w), a, b, raw);
+            unpack<T>(raw, w);
+        }
+    }
+    float dw[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[j] = 0.0f;
+    const float inv_dim = 1.0f / static_cast<float>(args.dim);
+
+    for (uint32_t item = block * kHeadWarps + warp; item < t.items; item += t.blocks * kHeadWarps) {
+        const uint32_t token = item / t.groups, group = item - token * t.groups;
+        const uint32_t bi = token / args.tokens, si = token - bi * args.tokens;
+
+        float c[4], s[4];
+        uint32_t turned = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            c[j] = 1.0f;
+            s[j] = 0.0f;
+            const int i = 4 * chunk + j;
+            if (i < args.pairs) {
+                const int64_t at = bi * args.pb + si * args.ps + axis[i] * args.pa;
+                double p;
+                if (args.pos_type == RTLYNX_POS_INT32)
+                    p = static_cast<double>(static_cast<const int32_t*>(args.positions)[at]);
+                else if (args.pos_type == RTLYNX_POS_INT64)
+                    p = static_cast<double>(static_cast<const int64_t*>(args.positions)[at]);
+                else
+                    p = static_cast<double>(static_cast<const float*>(args.positions)[at]);
+                double turn = p * turns[i];
+                turn -= rint(turn);
+                const double quarter = rint(4.0 * turn);
+                const float rest = static_cast<float>(turn - 0.25 * quarter);
+                float sn, cs;
+                sincospif(2.0f * rest, &sn, &cs);
+                const int q = static_cast<int>(quarter) & 3;
+                c[j] = q == 0 ? cs : (q == 1 ? -sn : (q == 2 ? -cs : sn));
+                s[j] = args.sin_sign * (q == 0 ? sn : (q == 1 ? cs : (q == 2 ? -sn : -cs)));
+                turned |= 1u << j;
+            }
+        }
+
+        const T* x = static_cast<const T*>(t.x) + bi * t.xb + si * t.xs;
+        const T* dy = KIND == kNormBackward ? static_cast<const T*>(t.dy) + bi * t.gb + si * t.gs : nullptr;
+        T* y = static_cast<T*>(t.y) + bi * t.yb + si * t.ys;
+        const uint32_t first = group * t.passes * kHeadsPerPass;
+        const uint32_t last = min(first + t.passes * kHeadsPerPass, t.heads);
+        for (uint32_t h0 = first; h0 < last; h0 += kHeadsPerPass * kUnroll) {
+            Raw<T> rx[kUnroll], rg[KIND == kNormBackward ? kUnroll : 1];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const uint32_t h = h0 + u * kHeadsPerPass + sub;
+#pragma unroll
+                for (int j = 0; j < static_cast<int>(2 * sizeof(T)); ++j) {
+                    rx[u].r[j] = 0u;
+                    if (KIND == kNormBackward) rg[u].r[j] = 0u;
+                }
+                if (active && h < last) {
+                    load8<T, HALF>(x + h * t.xh, a, b, rx[u]);
+                    if constexpr (KIND == kNormBackward) load8<T, HALF>(dy + h * t.gh, a, b, rg[u]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const uint32_t h = h0 + u * kHeadsPerPass + sub;
+                if (h0 + u * kHeadsPerPass >= last) break;  // the same in the whole warp
+                float v[8];
+                unpack<T>(rx[u], v);
+                if constexpr (KIND == kRope) {
+                    rotate<HALF>(v, c, s, turned);
+                } else {
+                    float squares = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) squares = fmaf(v[j], v[j], squares);
+                    const float r = rsqrtf(fmaf(head_sum<LANES>(squares), inv_dim, args.eps));
+                    if constexpr (KIND == kNorm) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] *= r * w[j];
+                        rotate<HALF>(v, c, s, turned);
+                    } else {
+                        float g[8];
+                        unpack<T>(rg[u], g);
+                        rotate<HALF>(g, c, s, turned);
+                        float dot = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            v[j] *= r;  // n
+                            dw[j] = fmaf(g[j], v[j], dw[j]);
+                            g[j] *= w[j];
+                            dot = fmaf(g[j], v[j], dot);
+                        }
+                        const float mean = head_sum<LANES>(dot) * inv_dim;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = r * fmaf(-v[j], mean, g[j]);
+                    }
+                }
+                if (active && h < last) {
+                    Raw<T> out;
+                    pack<T>(v, out);
+                    store8<T, HALF>(y + h * t.yh, a, b, out);
+                }
+            }
+        }
+    }
+
+    if constexpr (KIND == kNormBackward) {
+        // heads that shared a pass hold the same channels in different lanes
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+            for (int m = LANES; m < 32; m <<= 1) dw[j] += __shfl_xor_sync(0xFFFFFFFFu, dw[j], m);
+            if (sub == 0) sums[(warp * 32 + chunk) * 8 + j] = dw[j];
+        }
+        __syncthreads();
+        if (t.part && warp == 0 && sub == 0 && active) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float total = 0.0f;
+                for (int k = 0; k < kHeadWarps; ++k) total += sums[(k * 32 + chunk) * 8 + j];
+                t.part[static_cast<size_t>(block) * args.dim + (j < 4 ? a + j : b + j - 4)] = total;
+            }
+        }
+    }
+}
+
+// Adds the rows of partial sums: block (channel / 32, tensor); a warp takes
+// every eighth row, in order, then the warps' sums are added in order.
+struct WeightGradArgs {
+    const float* part[2];
+    float* dw[2];
+    uint32_t rows[2];
+    int dim;
+};
+
+__global__ void __launch_bounds__(kHeadThreads) rtlynx_heads_weight_grad_kernel(const WeightGradArgs args) {
+    __shared__ float sums[kHeadWarps][32];
+    grid_dependency_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.y, c = blockIdx.x * 32 + lane;
+    if (!args.dw[t]) return;
+    float total = 0.0f;
+    if (c < args.dim)
+        for (uint32_t r = warp; r < args.rows[t]; r += kHeadWarps)
+            total += args.part[t][static_cast<size_t>(r) * args.dim + c];
+    sums[warp][lane] = total;
+    __syncthreads();
+    if (warp == 0 && c < args.dim) {
+        float all = 0.0f;
+        for (int k = 0; k < kHeadWarps; ++k) all += sums[k][lane];
+        args.dw[t][c] = all;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+using Wide = __int128;
+
+bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// A view with the sizes it is used at.
+struct View {
+    const rtlynx_heads* v;
+    int64_t B, S, D;
+    int bytes;
+    Wide within() const { return Wide(S - 1) * v->stride_s + Wide(v->heads - 1) * v->stride_h + D; }  // one sequence
+    Wide token() const { return Wide(v->heads - 1) * v->stride_h + D; }
+    Wide extent() const { return Wide(B - 1) * v->stride_b + within(); }
+    Wide begin() const { return Wide(reinterpret_cast<uintptr_t>(v->ptr)); }
+    Wide end() const { return begin() + extent() * bytes; }
+};
+
+bool same_view(const View& a, const View& b) {
+    return a.v->ptr == b.v->ptr && a.v->heads == b.v->heads && (a.B == 1 || a.v->stride_b == b.v->stride_b) &&
+           (a.S == 1 || a.v->stride_s == b.v->stride_s) && (a.v->heads == 1 || a.v->stride_h == b.v->stride_h);
+}
+
+// Whether two views may share an element: their ranges meet, and they are not
+// seen to be different parts of the same rows (tokens or sequences).
+bool may_meet(const View& a, const View& b) {
+    if (a.end() <= b.begin() || b.end() <= a.begin()) return false;
+    const Wide bytes = b.begin() - a.begin();
+    if (bytes % a.bytes) return true;
+    const Wide delta = bytes / a.bytes;
+    auto apart = [&](Wide period, Wide ea, Wide eb) {
+        if (period <= 0) return false;
+        const Wide r = ((delta % period) + period) % period;
+        return r >= ea && r + eb <= period;
+    };
+    if (a.B > 1 && a.v->stride_b == b.v->stride_b && apart(a.v->stride_b, a.within(), b.within())) return false;
+    const int64_t s = a.v->stride_s;
+    if (a.S > 1 && s > 0 && s == b.v->stride_s &&
+        (a.B == 1 || (a.v->stride_b % s == 0 && b.v->stride_b % s == 0)) && apart(s, a.token(), b.token()))
+        return false;
+    return true;
+}
+
+// Whether an output view writes an element twice.
+bool self_overlap(const View& a) {
+    struct Dim {
+        int64_t n, stride;
+    } d[3] = {{a.B, a.v->stride_b}, {a.S, a.v->stride_s}, {a.v->heads, a.v->stride_h}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (d[j].stride < d[i].stride) {
+                const Dim t = d[i];
+                d[i] = d[j];
+                d[j] = t;
+            }
+    Wide span = a.D;
+    for (const Dim& k : d) {
+        if (k.n == 1) continue;
+        if (k.stride < span) return true;
+        span += Wide(k.n - 1) * k.stride;
+    }
+    return false;
+}
+
+int check_view(const View& a) {
+    if (!a.v->ptr || !aligned(a.v->ptr) || a.v->heads <= 0) return RTLYNX_ERR_INVALID_ARG;
+    const rtlynx_heads& v = *a.v;
+    auto bad = [](int64_t n, int64_t stride) { return n > 1 && (stride < 0 || stride % 8); };
+    if (bad(a.B, v.stride_b) || bad(a.S, v.stride_s) || bad(v.heads, v.stride_h)) return RTLYNX_ERR_INVALID_ARG;
+    if (v.heads > 65536 || a.extent() > (Wide(1) << 45)) return RTLYNX_ERR_UNSUPPORTED;
+    return RTLYNX_OK;
+}
+
+bool meets(const View& a, const void* p, Wide bytes) {
+    const Wide b = Wide(reinterpret_cast<uintptr_t>(p));
+    return p && bytes > 0 && a.begin() < b + bytes && b < a.end();
+}
+
+bool ranges_meet(const void* p, Wide np, const void* q, Wide nq) {
+    if (!p || !q) return false;
+    const Wide a = Wide(reinterpret_cast<uintptr_t>(p)), b = Wide(reinterpret_cast<uintptr_t>(q));
+    return a < b + nq && b < a + np;
+}
+
+int elem_bytes(int dtype) { return dtype == RTLYNX_FP32 ? 4 : 2; }
+
+int lanes_of(int64_t dim) { return dim <= 32 ? 4 : (dim <= 64 ? 8 : (dim <= 128 ? 16 : 32)); }
+
+// How a tensor's token-heads are dealt to warps.  A warp takes all heads of a
+// token, so that angles are computed once, unless that leaves fewer than
+// about 16 warps an SM: then a token's heads are cut into more, shorter runs.
+void deal(HeadTensor& t, int64_t rows, int64_t heads, int64_t dim, int num_sms, bool persistent) {
+    const int64_t per_pass = 32 / lanes_of(dim);
+    const int64_t all = (heads + per_pass - 1) / per_pass;
+    const int64_t want = 16ll * num_sms;
+    int64_t groups = rows >= want ? 1 : (want + rows - 1) / rows;
+    if (groups > all) groups = all;
+    t.passes = static_cast<uint32_t>((all + groups - 1) / groups);
+    t.groups = static_cast<uint32_t>((all + t.passes - 1) / t.passes);
+    t.heads = static_cast<uint32_t>(heads);
+    const int64_t items = rows * t.groups;
+    t.items = static_cast<uint32_t>(items);
+    int64_t blocks = (items + kHeadWarps - 1) / kHeadWarps;
+    // backward: a bounded number of blocks, each with one row of partial sums
+    int64_t most = 1ll << 30;
+    if (persistent) most = 2ll * num_sms < kHeadGradRows ? 2ll * num_sms : kHeadGradRows;
+    t.blocks = static_cast<uint32_t>(blocks < most ? blocks : most);
+}
+
+template <typename T, int LANES>
+int launch_lanes(const HeadArgs& args, bool half, int kind, cudaStream_t stream) {
+    const dim3 grid(args.t[0].blocks + args.t[1].blocks), block(kHeadThreads);
+    if (half) {
+        if (kind == kRope) return launch_dependent(rtlynx_heads_kernel<T, LANES, true, kRope>, grid, block, 0, stream, args);
+        if (kind == kNorm) return launch_dependent(rtlynx_heads_kernel<T, LANES, true, kNorm>, grid, block, 0, stream, args);
+        return launch_dependent(rtlynx_heads_kernel<T, LANES, true, kNormBackward>, grid, block, 0, stream, args);
+    }
+    if (kind == kRope) return launch_dependent(rtlynx_heads_kernel<T, LANES, false, kRope>, grid, block, 0, stream, args);
+    if (kind == kNorm) return launch_dependent(rtlynx_heads_kernel<T, LANES, false, kNorm>, grid, block, 0, stream, args);
+    return launch_dependent(rtlynx_heads_kernel<T, LANES, false, kNormBackward>, grid, block, 0, stream, args);
+}
+
+template <typename T>
+int launch_type(const HeadArgs& args, bool half, int kind, cudaStream_t stream) {
+    switch (lanes_of(args.dim)) {
+        case 4: return launch_lanes<T, 4>(args, half, kind, stream);
+        case 8: return launch_lanes<T, 8>(args, half, kind, stream);
+        case 16: return launch_lanes<T, 16>(args, half, kind, stream);
+        default: return launch_lanes<T, 32>(args, half, kind, stream);
+    }
+}
+
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct Call {
+    const rtlynx_heads *x[2], *dy[2], *y[2];  // queries, keys; keys NULL when the call has none
+    const void* w[2];
+    float* dw[2];
+};
+
+// Checks and runs one call of any kind.
+int run_heads(int kind, float sin_sign, const Call& call, int64_t B, int64_t S, int64_t D, int dtype,
+              const rtlynx_rope_spec* spec, const void* positions, int64_t pos_stride_b, int64_t pos_stride_s,
+              int64_t pos_stride_a, float eps, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    if (dtype != RTLYNX_BF16 && dtype != RTLYNX_FP16 && dtype != RTLYNX_FP32) return RTLYNX_ERR_INVALID_ARG;
+    if (B <= 0 || S <= 0 || D <= 0 || D % 8) return RTLYNX_ERR_INVALID_ARG;
+    if (D > kMaxDim || B > INT32_MAX || S > INT32_MAX || B * S > INT32_MAX) return RTLYNX_ERR_UNSUPPORTED;
+    if (!spec || !positions || !call.x[0] || !call.y[0]) return RTLYNX_ERR_INVALID_ARG;
+    if ((call.x[1] == nullptr) != (call.y[1] == nullptr)) return RTLYNX_ERR_INVALID_ARG;
+    if (kind == kNormBackward && (!call.dy[0] || (call.x[1] == nullptr) != (call.dy[1] == nullptr)))
+        return RTLYNX_ERR_INVALID_ARG;
+    if (kind != kRope && !(eps > 0.0f && eps < INFINITY)) return RTLYNX_ERR_INVALID_ARG;
+    // the rotation
+    if (spec->n_axes < 1) return RTLYNX_ERR_INVALID_ARG;
+    if (spec->n_axes > RTLYNX_MAX_AXES) return RTLYNX_ERR_UNSUPPORTED;
+    if (spec->pairing != RTLYNX_ROPE_INTERLEAVED && spec->pairing != RTLYNX_ROPE_HALF) return RTLYNX_ERR_INVALID_ARG;
+    if (spec->pos_type != RTLYNX_POS_INT32 && spec->pos_type != RTLYNX_POS_INT64 && spec->pos_type != RTLYNX_POS_FP32)
+        return RTLYNX_ERR_INVALID_ARG;
+    int64_t rotated = 0;
+    for (int a = 0; a < spec->n_axes; ++a) {
+        if (spec->axis_dim[a] < 2 || spec->axis_dim[a] % 2 || spec->axis_dim[a] > D) return RTLYNX_ERR_INVALID_ARG;
+        rotated += spec->axis_dim[a];
+    }
+    if (rotated > D) return RTLYNX_ERR_INVALID_ARG;
+    if (spec->pairing == RTLYNX_ROPE_HALF && rotated % 8) return RTLYNX_ERR_UNSUPPORTED;
+    if (!spec->inv_freq && !(spec->theta > 0.0 && spec->theta < INFINITY)) return RTLYNX_ERR_INVALID_ARG;
+    const uintptr_t pos_align = spec->pos_type == RTLYNX_POS_INT64 ? 8 : 4;
+    if (reinterpret_cast<uintptr_t>(positions) % pos_align) return RTLYNX_ERR_INVALID_ARG;
+    if ((B > 1 && pos_stride_b < 0) || (S > 1 && pos_stride_s < 0) || (spec->n_axes > 1 && pos_stride_a < 0))
+        return RTLYNX_ERR_INVALID_ARG;
+    const Wide pos_extent = Wide(B - 1) * pos_stride_b + Wide(S - 1) * pos_stride_s +
+                            Wide(spec->n_axes - 1) * pos_stride_a + 1;
+    if (pos_extent > (Wide(1) << 45)) return RTLYNX_ERR_UNSUPPORTED;
+    const Wide pos_bytes = pos_extent * Wide(pos_align);
+
+    // the tensors
+    const int bytes = elem_bytes(dtype);
+    const int tensors = call.x[1] ? 2 : 1;
+    auto view = [&](const rtlynx_heads* v) { return View{v, B, S, D, bytes}; };
+    for (int t = 0; t < tensors; ++t) {
+        const rtlynx_heads* used[3] = {call.x[t], call.y[t], kind == kNormBackward ? call.dy[t] : nullptr};
+        for (const rtlynx_heads* v : used) {
+            if (!v) continue;
+            const int rc = check_view(view(v));
+            if (rc) return rc;
+            if (v->heads != call.x[t]->heads) return RTLYNX_ERR_INVALID_ARG;
+        }
+        if (call.w[t] && !aligned(call.w[t])) return RTLYNX_ERR_INVALID_ARG;
+        if (call.dw[t] && !aligned(call.dw[t])) return RTLYNX_ERR_INVALID_ARG;
+        if (self_overlap(view(call.y[t]))) return RTLYNX_ERR_INVALID_ARG;
+    }
+    // An output may be exactly its own input (or incoming gradient); it may
+    // share no element with anything else.
+    for (int t = 0; t < tensors; ++t) {
+        const View y = view(call.y[t]);
+        for (int o = 0; o < tensors; ++o) {
+            const View x = view(call.x[o]);
+            if (!(o == t && same_view(y, x)) && may_meet(y, x)) return RTLYNX_ERR_INVALID_ARG;
+            if (kind == kNormBackward) {
+                const View g = view(call.dy[o]);
+                if (!(o == t && same_view(y, g)) && may_meet(y, g)) return RTLYNX_ERR_INVALID_ARG;
+            }
+            if (o != t && may_meet(y, view(call.y[o]))) return RTLYNX_ERR_INVALID_ARG;
+            if (meets(y, call.w[o], Wide(D) * bytes) || meets(y, call.dw[o], Wide(D) * 4)) return RTLYNX_ERR_INVALID_ARG;
+        }
+        if (meets(y, positions, pos_bytes)) return RTLYNX_ERR_INVALID_ARG;
+    }
+
+    HeadArgs args{};
+    const bool grads = kind == kNormBackward && (call.dw[0] || call.dw[1]);
+    size_t need = 0;
+    if (grads) {
+        need = rtlynx_qk_norm_rope_workspace_size(D);
+        if (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+            return RTLYNX_ERR_INVALID_ARG;
+        for (int t = 0; t < tensors; ++t) {
+            const rtlynx_heads* used[3] = {call.x[t], call.y[t], call.dy[t]};
+            for (const rtlynx_heads* v : used)
+                if (meets(view(v), workspace, Wide(need))) return RTLYNX_ERR_INVALID_ARG;
+            const rtlynx_heads* read[2] = {call.x[t], call.dy[t]};
+            for (int o = 0; o < tensors; ++o) {
+                for (const rtlynx_heads* v : read)
+                    if (meets(view(v), call.dw[o], Wide(D) * 4)) return RTLYNX_ERR_INVALID_ARG;
+                if (ranges_meet(call.dw[t], Wide(D) * 4, call.w[o], Wide(D) * bytes)) return RTLYNX_ERR_INVALID_ARG;
+            }
+            if (ranges_meet(call.w[t], Wide(D) * bytes, workspace, Wide(need)) ||
+                ranges_meet(call.dw[t], Wide(D) * 4, workspace, Wide(need)) ||
+                ranges_meet(call.dw[t], Wide(D) * 4, positions, pos_bytes))
+                return RTLYNX_ERR_INVALID_ARG;
+        }
+        if (ranges_meet(call.dw[0], Wide(D) * 4, call.dw[1], Wide(D) * 4) ||
+            ranges_meet(positions, pos_bytes, workspace, Wide(need)))
+            return RTLYNX_ERR_INVALID_ARG;
+    }
+    int num_sms = 0;
+    int* err = nullptr;
+    const int rc = device_info(&num_sms, &err);
+    if (rc) return rc;
+
+    for (int t = 0; t < tensors; ++t) {
+        HeadTensor& h = args.t[t];
+        h.x = call.x[t]->ptr;
+        h.xb = call.x[t]->stride_b, h.xs = call.x[t]->stride_s, h.xh = call.x[t]->stride_h;
+        h.y = call.y[t]->ptr;
+        h.yb = call.y[t]->stride_b, h.ys = call.y[t]->stride_s, h.yh = call.y[t]->stride_h;
+        if (kind == kNormBackward) {
+            h.dy = call.dy[t]->ptr;
+            h.gb = call.dy[t]->stride_b, h.gs = call.dy[t]->stride_s, h.gh = call.dy[t]->stride_h;
+        }
+        h.w = call.w[t];
+        const int64_t rows = B * S;
+        const int64_t passes = (call.x[t]->heads * lanes_of(D) + 31) / 32;
+        if (rows * passes > (int64_t(1) << 31)) return RTLYNX_ERR_UNSUPPORTED;  // items fit 32 bits whatever the deal
+        deal(h, rows, call.x[t]->heads, D, num_sms, kind == kNormBackward);
+        if (call.dw[t])
+            h.part = static_cast<float*>(workspace) + static_cast<size_t>(t) * kHeadGradRows * D;
+    }
+    args.positions = positions;
+    args.pb = pos_stride_b, args.ps = pos_stride_s, args.pa = pos_stride_a;
+    args.pos_type = spec->pos_type;
+    args.tokens = static_cast<uint32_t>(S);
+    args.dim = static_cast<int>(D);
+    args.pairs = static_cast<int>(rotated / 2);
+    args.eps = eps;
+    args.sin_sign = sin_sign;
+    for (int a = 0, i = 0; a < spec->n_axes; ++a)
+        for (int j = 0; j < spec->axis_dim[a] / 2; ++j, ++i) {
+            args.axis[i] = static_cast<uint8_t>(a);
+            const double f = spec->inv_freq ? spec->inv_freq[i] : pow(spec->theta, -2.0 * j / spec->axis_dim[a]);
+            args.turns[i] = f / kTwoPi;
+        }
+    const bool half = spec->pairing == RTLYNX_ROPE_HALF;
+    int e = dtype == RTLYNX_BF16   ? launch_type<__nv_bfloat16>(args, half, kind, stream)
+            : dtype == RTLYNX_FP16 ? launch_type<__half>(args, half, kind, stream)
+                                   : launch_type<float>(args, half, kind, stream);
+    if (e) return RTLYNX_ERR_CUDA;
+    if (grads) {
+        WeightGradArgs wg{};
+        wg.dim = static_cast<int>(D);
+        for (int t = 0; t < tensors; ++t) {
+            wg.part[t] = args.t[t].part;
+            wg.dw[t] = call.dw[t];
+            wg.rows[t] = args.t[t].blocks;
+        }
+        e = launch_dependent(rtlynx_heads_weight_grad_kernel, dim3((D + 31) / 32, 2), dim3(kHeadThreads), 0, stream, wg);
+        if (e) return RTLYNX_ERR_CUDA;
+    }
+    return RTLYNX_OK;
+}
+
+}  // namespace
+}  // namespace rtlynx
+
+using namespace rtlynx;
+
+extern "C" {
+
+int rtlynx_rope(const rtlynx_heads* q, const rtlynx_heads* k, const rtlynx_heads* q_out, const rtlynx_heads* k_out,
+                int64_t B, int64_t S, int64_t D_head, int dtype, const rtlynx_rope_spec* spec, const void* positions,
+                int64_t pos_stride_b, int64_t pos_stride_s, int64_t pos_stride_a, void* stream) {
+    const Call call{{q, k}, {nullptr, nullptr}, {q_out, k_out}, {nullptr, nullptr}, {nullptr, nullptr}};
+    return run_heads(kRope, 1.0f, call, B, S, D_head, dtype, spec, positions, pos_stride_b, pos_stride_s, pos_stride_a,
+                     0.0f, nullptr, 0, static_cast<cudaStream_t>(stream));
+}
+
+int rtlynx_rope_backward(const rtlynx_heads* dq_out, const rtlynx_heads* dk_out, const rtlynx_heads* dq,
+                         const rtlynx_heads* dk, int64_t B, int64_t S, int64_t D_head, int dtype,
+                         const rtlynx_rope_spec* spec, const void* positions, int64_t pos_stride_b,
+                         int64_t pos_stride_s, int64_t pos_stride_a, void* stream) {
+    const Call call{{dq_out, dk_out}, {nullptr, nullptr}, {dq, dk}, {nullptr, nullptr}, {nullptr, nullptr}};
+    return run_heads(kRope, -1.0f, call, B, S, D_head, dtype, spec, positions, pos_stride_b, pos_stride_s, pos_stride_a,
+                     0.0f, nullptr, 0, static_cast<cudaStream_t>(stream));
+}
+
+int rtlynx_qk_norm_rope(const rtlynx_heads* q, const rtlynx_heads* k, const void* w_q, const void* w_k,
+                        const rtlynx_heads* q_out, const rtlynx_heads* k_out, int64_t B, int64_t S, int64_t D_head,
+                        int dtype, float eps, const rtlynx_rope_spec* spec, const void* positions,
+                        int64_t pos_stride_b, int64_t pos_stride_s, int64_t pos_stride_a, void* stream) {
+    const Call call{{q, k}, {nullptr, nullptr}, {q_out, k_out}, {w_q, k ? w_k : nullptr}, {nullptr, nullptr}};
+    return run_heads(kNorm, 1.0f, call, B, S, D_head, dtype, spec, positions, pos_stride_b, pos_stride_s, pos_stride_a,
+                     eps, nullptr, 0, static_cast<cudaStream_t>(stream));
+}
+
+size_t rtlynx_qk_norm_rope_workspace_size(int64_t D_head) {
+    if (D_head <= 0 || D_head % 8 || D_head > kMaxDim) return 0;
+    return round256(2 * static_cast<size_t>(kHeadGradRows) * static_cast<size_t>(D_head) * sizeof(float));
+}
+
+int rtlynx_qk_norm_rope_backward(const rtlynx_heads* dq_out, const rtlynx_heads* dk_out, const rtlynx_heads* q,
+                                 const rtlynx_heads* k, const void* w_q, const void* w_k, const rtlynx_heads* dq,
+                                 const rtlynx_heads* dk, float* dw_q, float* dw_k, int64_t B, int64_t S,
+                                 int64_t D_head, int dtype, float eps, const rtlynx_rope_spec* spec,
+                                 const void* positions, int64_t pos_stride_b, int64_t pos_stride_s,
+                                 int64_t pos_stride_a, void* workspace, size_t ws_bytes, void* stream) {
+    const Call call{{q, k}, {dq_out, dk_out}, {dq, dk}, {w_q, k ? w_k : nullptr}, {dw_q, k ? dw_k : nullptr}};
+    return run_heads(kNormBackward, -1.0f, call, B, S, D_head, dtype, spec, positions, pos_stride_b, pos_stride_s,
+                     pos_stride_a, eps, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

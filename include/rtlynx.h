@@ -12,7 +12,8 @@
  *           sparse GEMM run in fused GPU kernels; the sparse and LoRA products
  *           are accumulated on chip.
  *
- * Conventions for every entry point:
+ * Conventions for every entry point (the query and key heads' entry points
+ * say where they take other types and strides):
  *   - Tensors are row-major bf16 (IEEE binary16-brain, little endian):
  *       X [M, D_in], W [D_out, D_in] (nn.Linear layout), L_A [D_out, R],
  *       L_B [R, D_in], Y [M, D_out].
@@ -194,6 +195,108 @@ int rtlynx_linear_host(const void* X_host, const void* W, const void* L_A, const
 int rtlynx_mlp_block(const void* X, const void* W_up, const void* LA_up, const void* LB_up, const void* W_down,
                      const void* LA_down, const void* LB_down, void* H, void* Y, int64_t M, int64_t D, int64_t D_ff,
                      int64_t R, int mode_up, int mode_down, void* stream);
+
+/* ---------------------------------------------------------------- query and key heads
+ * What stands between the qkv layer and attention in a transformer block:
+ * rotary positions with several axes (time, height and width of a video
+ * latent, row and column of an image, or the one axis of a text), the RMS norm
+ * of each head fused with them, and the gradients of both.
+ *
+ *   rope          y = R(p) x
+ *   qk_norm_rope  y = R(p) (w * x r),   r = (mean_c x_c^2 + eps)^(-1/2)
+ *
+ * R(p) turns pair i of a head by p[axis(i)] * f_i radians, (x0, x1) -> (x0 cos -
+ * x1 sin, x0 sin + x1 cos).  The head's first sum(axis_dim) channels are
+ * turned, the rest pass through.  The pairs of axis a follow those of axis
+ * a - 1; pair j of an axis of d channels has f = theta^(-2 j / d), or
+ * inv_freq[i] where the caller gives frequencies of its own.
+ * Angles are taken to one turn in 64 bits, so far positions lose nothing;
+ * everything else is in 32, each output rounded once.
+ */
+typedef enum { RTLYNX_BF16 = 0, RTLYNX_FP16 = 1, RTLYNX_FP32 = 2 } rtlynx_dtype;
+
+typedef enum {
+    RTLYNX_ROPE_INTERLEAVED = 0,  /* pair i = channels 2 i, 2 i + 1 */
+    RTLYNX_ROPE_HALF = 1          /* pair i = channels i, i + sum(axis_dim) / 2 */
+} rtlynx_rope_pairing;
+
+typedef enum { RTLYNX_POS_INT32 = 0, RTLYNX_POS_INT64 = 1, RTLYNX_POS_FP32 = 2 } rtlynx_pos_type;
+
+#define RTLYNX_MAX_AXES 4
+
+/* The rotation; read on the host before the call returns. */
+typedef struct {
+    int32_t n_axes;                    /* 1 .. RTLYNX_MAX_AXES */
+    int32_t axis_dim[RTLYNX_MAX_AXES]; /* channels of each axis, even, >= 2 */
+    int32_t pairing;                   /* rtlynx_rope_pairing */
+    int32_t pos_type;                  /* rtlynx_pos_type of the positions */
+    double theta;                      /* > 0 and finite; unused with inv_freq */
+    const double* inv_freq;            /* host, sum(axis_dim) / 2 values, or NULL */
+} rtlynx_rope_spec;
+
+/* Heads in device memory: channel c of head h of token s of sequence b is at
+ * ptr + b stride_b + s stride_s + h stride_h + c, in elements.  The strides
+ * are multiples of 8 and >= 0 (where there is one sequence, token or head its
+ * stride is not looked at), ptr is 16-byte aligned.  An input may have a
+ * stride of 0 (broadcast); an output may not write an element twice. */
+typedef struct {
+    void* ptr;
+    int64_t heads;  /* 1 .. 65536 */
+    int64_t stride_b, stride_s, stride_h;
+} rtlynx_heads;
+
+/*
+ * rtlynx_rope, rtlynx_qk_norm_rope - queries and keys in one launch.
+ *   q, k          inputs, B sequences of S tokens, D_head channels a head (a
+ *                 multiple of 8 up to 256); k and k_out may both be NULL
+ *   q_out, k_out  outputs with as many heads.  q_out may be exactly q (in
+ *                 place), k_out exactly k; an output that may share an element
+ *                 with anything else is refused.  Parts of one packed buffer
+ *                 are told apart when their token (or sequence) strides agree.
+ *   w_q, w_k      [D_head] of the same type, or NULL for ones
+ *   positions     device; the position of token s of sequence b on axis a is at
+ *                 b pos_stride_b + s pos_stride_s + a pos_stride_a (>= 0)
+ *   dtype         rtlynx_dtype of q, k, w and the outputs
+ *   eps           > 0 and finite
+ * RTLYNX_ERR_INVALID_ARG: a size <= 0, D_head not a multiple of 8, axes that
+ * are odd or exceed the head, an argument out of its list, or a pointer,
+ * stride or overlap against the rules above.  RTLYNX_ERR_UNSUPPORTED: D_head >
+ * 256, more than four axes, half pairing with sum(axis_dim) not a multiple of
+ * 8, or B * S * heads beyond 2^31.
+ */
+int rtlynx_rope(const rtlynx_heads* q, const rtlynx_heads* k, const rtlynx_heads* q_out, const rtlynx_heads* k_out,
+                int64_t B, int64_t S, int64_t D_head, int dtype, const rtlynx_rope_spec* spec, const void* positions,
+                int64_t pos_stride_b, int64_t pos_stride_s, int64_t pos_stride_a, void* stream);
+
+int rtlynx_qk_norm_rope(const rtlynx_heads* q, const rtlynx_heads* k, const void* w_q, const void* w_k,
+                        const rtlynx_heads* q_out, const rtlynx_heads* k_out, int64_t B, int64_t S, int64_t D_head,
+                        int dtype, float eps, const rtlynx_rope_spec* spec, const void* positions,
+                        int64_t pos_stride_b, int64_t pos_stride_s, int64_t pos_stride_a, void* stream);
+
+/* Gradients.  dq_out, dk_out are the gradients of the outputs; dq, dk receive
+ * those of the inputs and may be exactly dq_out and dk_out, or (norm form)
+ * exactly q and k.  The rotation alone needs no inputs:
+ *   rope          dx = R(p)^T dy
+ *   qk_norm_rope  g = R(p)^T dy, n = x r:  dx = r (g w - n mean_c(g w n)),
+ *                 dw = sum of g n over every token and head
+ * dw_q, dw_k are [D_head] float and may be NULL.  The sums run in a fixed
+ * order, so equal calls on one kind of GPU give equal bits.  With dw_q or
+ * dw_k the call needs a device workspace of
+ * rtlynx_qk_norm_rope_workspace_size(D_head) bytes (0 for an invalid D_head),
+ * 256-byte aligned, for itself until it has finished. */
+int rtlynx_rope_backward(const rtlynx_heads* dq_out, const rtlynx_heads* dk_out, const rtlynx_heads* dq,
+                         const rtlynx_heads* dk, int64_t B, int64_t S, int64_t D_head, int dtype,
+                         const rtlynx_rope_spec* spec, const void* positions, int64_t pos_stride_b,
+                         int64_t pos_stride_s, int64_t pos_stride_a, void* stream);
+
+size_t rtlynx_qk_norm_rope_workspace_size(int64_t D_head);
+
+int rtlynx_qk_norm_rope_backward(const rtlynx_heads* dq_out, const rtlynx_heads* dk_out, const rtlynx_heads* q,
+                                 const rtlynx_heads* k, const void* w_q, const void* w_k, const rtlynx_heads* dq,
+                                 const rtlynx_heads* dk, float* dw_q, float* dw_k, int64_t B, int64_t S,
+                                 int64_t D_head, int dtype, float eps, const rtlynx_rope_spec* spec,
+                                 const void* positions, int64_t pos_stride_b, int64_t pos_stride_s,
+                                 int64_t pos_stride_a, void* workspace, size_t ws_bytes, void* stream);
 
 /* Largest workspace rtlynx_linear_noalloc can use (32 MiB). */
 #define RTLYNX_NOALLOC_MAX_BYTES (32u << 20)
