@@ -9,6 +9,7 @@ stream handle (int) or a ``torch.cuda.Stream``.
     Y = S(X) W^T + X (L_A L_B)^T        mode = MODE_SPARSE
     Y = X W^T                           mode = MODE_DENSE_SKIP
     H = GELU(up(X)), Y = down(H)        rtlynx_mlp_block (two such layers)
+    Y = down(act(gate(X)) * up(X))      rtlynx_gated_mlp_block
     R(p) x,  R(p) (w x / rms(x))        rtlynx_rope, rtlynx_qk_norm_rope (query and key heads)
 
 (RT-Lynx summary page, four-step pipeline paragraph, steps 1-3.)
@@ -34,6 +35,7 @@ ERR_CUDA = 3
 ERR_OOM = 4
 ERR_DEVICE_TIMEOUT = 5
 
+ACT_SILU, ACT_GELU = 0, 1                     # rtlynx_act
 BF16, FP16, FP32 = 0, 1, 2                    # rtlynx_dtype
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1            # rtlynx_rope_pairing
 POS_INT32, POS_INT64, POS_FP32 = 0, 1, 2      # rtlynx_pos_type
@@ -46,6 +48,7 @@ ABI_SYMBOLS = (
     "rtlynx_sparsify_debug", "rtlynx_linear_host", "rtlynx_mlp_block", "rtlynx_linear_noalloc",
     "rtlynx_kernel_launches", "rtlynx_schedule_info",
     "rtlynx_quantize_weight_fp8", "rtlynx_linear_fp8", "rtlynx_linear_fp8_events", "rtlynx_sparsify_fp8_debug",
+    "rtlynx_gated_mlp_block", "rtlynx_gated_mlp_backward_workspace_size", "rtlynx_gated_mlp_backward",
     "rtlynx_rope", "rtlynx_rope_backward", "rtlynx_qk_norm_rope", "rtlynx_qk_norm_rope_workspace_size",
     "rtlynx_qk_norm_rope_backward",
     "rtlynx_wait_selftest", "rtlynx_stream_status", "rtlynx_status_string", "rtlynx_release",
@@ -126,6 +129,12 @@ def lib() -> ctypes.CDLL:
         L.rtlynx_kernel_launches.restype = i
         L.rtlynx_schedule_info.argtypes = [i64, i64, i64, i64, i, ctypes.POINTER(Schedule)]
         L.rtlynx_schedule_info.restype = i
+        L.rtlynx_gated_mlp_block.argtypes = [p] * 10 + [i64, i64, i64, i64, i, i, p]
+        L.rtlynx_gated_mlp_block.restype = i
+        L.rtlynx_gated_mlp_backward_workspace_size.argtypes = [i64, i64, i64]
+        L.rtlynx_gated_mlp_backward_workspace_size.restype = ctypes.c_size_t
+        L.rtlynx_gated_mlp_backward.argtypes = [p] * 12 + [i64, i64, i64, i, p, ctypes.c_size_t, p]
+        L.rtlynx_gated_mlp_backward.restype = i
         hv, spec, f = ctypes.POINTER(HeadsView), ctypes.POINTER(RopeSpec), ctypes.c_float
         L.rtlynx_rope.argtypes = [hv, hv, hv, hv, i64, i64, i64, i, spec, p, i64, i64, i64, p]
         L.rtlynx_rope.restype = i
@@ -263,6 +272,26 @@ def rtlynx_linear_fp8_events(X, W8, qw, L_A8, L_B, Y, M, D_in, D_out, R, ev_star
 def rtlynx_sparsify_fp8_debug(X, M, D_in, codes, meta, qx, stream=None) -> int:
     return _check(lib().rtlynx_sparsify_fp8_debug(_ptr(X), M, D_in, _ptr(codes), _ptr(meta), _ptr(qx),
                                                   _stream(stream)), "rtlynx_sparsify_fp8_debug")
+
+
+def rtlynx_gated_mlp_block(X, W_gate, W_up, W_down, LA_down, LB_down, G, U, H, Y, M, D, D_ff, R, act=ACT_SILU,
+                           mode_down=MODE_DENSE_SKIP, stream=None) -> int:
+    """H = act(X W_gate^T) * (X W_up^T) [M, D_ff], Y = layer_down(H) [M, D]; see include/rtlynx.h."""
+    return _check(lib().rtlynx_gated_mlp_block(_ptr(X), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _ptr(LA_down),
+                                               _ptr(LB_down), _ptr(G), _ptr(U), _ptr(H), _ptr(Y), M, D, D_ff, R, act,
+                                               mode_down, _stream(stream)), "rtlynx_gated_mlp_block")
+
+
+def rtlynx_gated_mlp_backward_workspace_size(M, D, D_ff) -> int:
+    return int(lib().rtlynx_gated_mlp_backward_workspace_size(M, D, D_ff))
+
+
+def rtlynx_gated_mlp_backward(dY, X, W_gate, W_up, W_down, G, U, H, dX, dW_gate, dW_up, dW_down, M, D, D_ff, act,
+                              workspace, ws_bytes, stream=None) -> int:
+    return _check(lib().rtlynx_gated_mlp_backward(_ptr(dY), _ptr(X), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _ptr(G),
+                                                  _ptr(U), _ptr(H), _ptr(dX), _ptr(dW_gate), _ptr(dW_up),
+                                                  _ptr(dW_down), M, D, D_ff, act, _ptr(workspace), ws_bytes,
+                                                  _stream(stream)), "rtlynx_gated_mlp_backward")
 
 
 def rtlynx_rope(q, k, q_out, k_out, B, S, D_head, dtype, spec, positions, pos_strides, stream=None) -> int:
@@ -531,3 +560,61 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, w_q, w_k, positions, rope, eps=1
                                      None if k is None else _heads_view(dk, q, "dk"), dw_q, dw_k, B, S, D, code, eps,
                                      spec, positions, strides, ws, ws_bytes, handle)
     return dq, dk, dw_q, dw_k
+
+
+def _matrix(t, shape, device, what):
+    """t, checked: a contiguous bf16 CUDA matrix of this shape on this device."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous bf16 {shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _gated_sizes(X, W_gate, W_up, W_down):
+    if not X.is_cuda or X.dim() != 2 or W_gate.dim() != 2:
+        raise ValueError("X [M, D] and W_gate [D_ff, D] are CUDA matrices")
+    (M, D), D_ff = X.shape, W_gate.shape[0]
+    _matrix(X, (M, D), X.device, "X")
+    _matrix(W_gate, (D_ff, D), X.device, "W_gate")
+    _matrix(W_up, (D_ff, D), X.device, "W_up")
+    _matrix(W_down, (D, D_ff), X.device, "W_down")
+    return M, D, D_ff
+
+
+def gated_mlp(X, W_gate, W_up, W_down, act=ACT_SILU, L_A=None, L_B=None, mode_down=MODE_DENSE_SKIP, save=False,
+              out=None, stream=None):
+    """Y [M, D] of the gated feed-forward block, for contiguous bf16 CUDA tensors X [M, D], W_gate and W_up [D_ff, D],
+    W_down [D, D_ff].
+
+    With mode_down=MODE_SPARSE the down-projection is the activation-sparse layer with the LoRA pair L_A [D, R],
+    L_B [R, D_ff].  With save=True the result is (Y, saved), saved = (G, U, H) for gated_mlp_backward."""
+    import torch
+    M, D, D_ff = _gated_sizes(X, W_gate, W_up, W_down)
+    R = 0 if (L_A is None or L_B is None or mode_down == MODE_DENSE_SKIP) else L_B.shape[0]
+    if R:
+        _matrix(L_A, (D, R), X.device, "L_A")
+        _matrix(L_B, (R, D_ff), X.device, "L_B")
+    with _Launch(X.device, stream) as handle:
+        Y = torch.empty((M, D), dtype=X.dtype, device=X.device) if out is None else _matrix(out, (M, D), X.device, "out")
+        H = torch.empty((M, D_ff), dtype=X.dtype, device=X.device)
+        G, U = (torch.empty_like(H), torch.empty_like(H)) if save else (None, None)
+        rtlynx_gated_mlp_block(X, W_gate, W_up, W_down, L_A if R else None, L_B if R else None, G, U, H, Y, M, D, D_ff,
+                               R, act, mode_down, handle)
+    return (Y, (G, U, H)) if save else Y
+
+
+def gated_mlp_backward(dY, X, W_gate, W_up, W_down, saved, act=ACT_SILU, needs=(True, True, True, True), stream=None):
+    """(dX, dW_gate, dW_up, dW_down) of gated_mlp with a dense down-projection, from dY [M, D] and its `saved`.
+
+    needs: which of the four to compute; the others are None."""
+    import torch
+    M, D, D_ff = _gated_sizes(X, W_gate, W_up, W_down)
+    _matrix(dY, (M, D), X.device, "dY")
+    for t, name in zip(saved, "GUH"):
+        _matrix(t, (M, D_ff), X.device, name)
+    with _Launch(X.device, stream) as handle:
+        grads = tuple(torch.empty_like(t) if need else None for t, need in zip((X, W_gate, W_up, W_down), needs))
+        ws_bytes = rtlynx_gated_mlp_backward_workspace_size(M, D, D_ff)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=X.device)
+        rtlynx_gated_mlp_backward(dY, X, W_gate, W_up, W_down, *saved, *grads, M, D, D_ff, act, ws, ws_bytes, handle)
+    return grads

@@ -1,0 +1,715 @@
+// Gated feed-forward block for sm_100a, forward and backward.
+//
+//   G = X Wg^T,  U = X Wu^T,  H = act(G) * U        one kernel
+//   Y = H Wd^T                                      the linear layer (gemm.cu)
+//   backward:
+//   dH = dY Wd,  dG = dH U act'(G),  dU = dH act(G) one kernel
+//   dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X,  dWd = dY^T H
+//                                                   one kernel for all four
+//
+// All of it is GEMM work, bound by the tensor cores but for few tokens.  One
+// persistent kernel template serves the three launches: a CTA pair computes
+// 256 x 256 of fp32 accumulator with cta_group::2 MMAs, each CTA holding 128
+// rows of A and 128 of B, with the accumulator double-buffered in tensor
+// memory so that the epilogue of one tile overlaps the main loop of the next.
+// Warp 0 loads by TMA, warp 1 issues the MMAs, the others run the epilogue.
+//
+// Gate and up projections in one kernel: CTA 0's half of B is 128 rows of Wg,
+// CTA 1's the same 128 rows of Wu.  The pair's MMA then leaves G in columns
+// 0-127 and U in 128-255 of the same tensor-memory rows, so the thread that
+// reads G[m, j] reads U[m, j] too: the activation and the product need no
+// exchange, and X is read once for both.
+//
+// Operands come in the layout they are stored in: "K-major" rows (X, Wg) or
+// "MN-major" where the reduction runs down the rows (dG^T X sums over tokens;
+// dY Wd over Wd's rows).  No transposed copy is made: the tensor map's box is
+// 64 contiguous elements by 64 rows either way, and the MMA's descriptors say
+// which of the two is K.
+//
+// fp32 accumulation throughout.  G, U, H, dG and dU are rounded to bf16 once:
+// they are the operands of the next MMA (which takes bf16), and what backward
+// keeps.  H is made from the unrounded G and U.
+#include "../../include/rtlynx.h"
+#include "act.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace rtlynx {
+namespace {
+
+constexpr uint32_t kTmemColumns = 512;
+constexpr int kTile = 256;                      // rows and accumulator columns of a tile
+constexpr int kHalf = 128;                      // one CTA's share of either operand
+constexpr int kOperandBytes = kHalf * 64 * 2;   // 128 x 64 values
+constexpr int kStageBytes = 2 * kOperandBytes;  // A and B
+constexpr int kStages = 6;
+constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 1024;
+constexpr int kMaxProblems = 4;
+constexpr int kMaxMaps = 12;
+
+enum Epilogue { kStore = 0, kGatedForward = 1, kGatedBackward = 2 };
+
+// One product A B^T (+ A' B'^T) of a launch.  Map indices point into
+// GatedArgs::maps; with b_by_rank CTA 1 uses the map after b0.
+struct Problem {
+    int m_pairs, n_tiles, group_n;
+    int first_unit, split;      // units [first_unit, first_unit + tiles * split)
+    int k0, k;                  // stages of the first operand pair, of both
+    int a0, b0, a1, b1;
+    int a_mn, b_mn;             // operand is MN-major
+    int rows, cols;             // of the output
+    uint16_t* out[3];           // forward: H, G, U (G, U may be null); backward: dG, dU; store: the output
+    const uint16_t* in[2];      // backward: G, U
+    float* part;                // split > 1: fp32 partial tiles
+};
+
+struct GatedArgs {
+    CUtensorMap maps[kMaxMaps];
+    Problem p[kMaxProblems];
+    int problems, units;
+    int act;
+    int* err;
+};
+
+struct Unit {
+    int problem, mp, nt, kb, ke, part;
+};
+
+__device__ __forceinline__ bool unit_at(int u, const GatedArgs& args, Unit& w) {
+    if (u >= args.units) return false;
+    int i = 0;
+    while (i + 1 < args.problems && u >= args.p[i + 1].first_unit) ++i;
+    const Problem& p = args.p[i];
+    const int local = u - p.first_unit;
+    const int tile = local / p.split;
+    w.problem = i;
+    w.part = local - tile * p.split;
+    w.kb = static_cast<int>(static_cast<int64_t>(w.part) * p.k / p.split);
+    w.ke = static_cast<int>(static_cast<int64_t>(w.part + 1) * p.k / p.split);
+    // column tiles in groups of group_n, a group's tiles row pair by row pair
+    const int per_group = p.m_pairs * p.group_n;
+    const int g = tile / per_group;
+    const int width = min(p.group_n, p.n_tiles - g * p.group_n);
+    const int in_group = tile - g * per_group;
+    w.mp = in_group / width;
+    w.nt = g * p.group_n + in_group % width;
+    return true;
+}
+
+__device__ __forceinline__ bool whole_warp_wait(uint64_t* bar, uint32_t parity, int* err) {
+    uint32_t ok = 0;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, err) ? 1u : 0u;
+    return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+
+// 128 x 64 values into shared memory, 128B swizzle.  K-major: 128 rows of 64
+// K values.  MN-major: two boxes of 64 row values x 64 K.
+__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, uint32_t bar, bool mn, int k,
+                                             int row) {
+    if (mn) {
+        tma_load_2d_pair(dst, map, bar, row, k);
+        tma_load_2d_pair(dst + kOperandBytes / 2, map, bar, row + 64, k);
+    } else {
+        tma_load_2d_pair(dst, map, bar, k, row);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+}
+
+__device__ __forceinline__ void unpack8(uint4 u, float* v) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+// Epilogue warps: four, or eight where the epilogue's own memory traffic would
+// otherwise outlast the main loop it overlaps; then two warps share a
+// quadrant of tensor-memory lanes and take half of the columns each.
+template <int EPI>
+struct Shape {
+    static constexpr int kEpiWarps = EPI == kStore ? 4 : 8;
+    static constexpr int kThreads = 64 + 32 * kEpiWarps;
+};
+
+template <int EPI, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads, 1)
+    rtlynx_gated_gemm_kernel(const __grid_constant__ GatedArgs args) {
+    constexpr int kEpiWarps = Shape<EPI>::kEpiWarps;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+    uint64_t* empty = full + kStages;
+    uint64_t* acc_full = empty + kStages;  // [2]
+    uint64_t* acc_empty = acc_full + 2;    // [2], used in the leader only
+    uint64_t* done_bar = acc_empty + 2;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+    int* err = args.err;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 2 * kEpiWarps);
+        }
+        mbar_init(done_bar, 1);
+        fence_mbar_init();
+        for (int i = 0; i < args.problems; ++i) {
+            prefetch_tmap(&args.maps[args.p[i].a0]);
+            prefetch_tmap(&args.maps[args.p[i].b0 + (EPI == kGatedForward ? static_cast<int>(rank) : 0)]);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_holder, kTmemColumns);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    grid_dependency_wait();
+
+    Unit w;
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = pair; ok && unit_at(u, args, w); u += num_pairs) {
+                const Problem& p = args.p[w.problem];
+                const int row0 = w.mp * kTile + static_cast<int>(rank) * kHalf;
+                const int col0 = EPI == kGatedForward ? w.nt * kHalf : w.nt * kTile + static_cast<int>(rank) * kHalf;
+                const bool a_mn = p.a_mn, b_mn = p.b_mn;
+                for (int kt = w.kb; kt < w.ke; ++kt) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1u, err)) {
+                        ok = false;
+                        break;
+                    }
+                    const bool second = kt >= p.k0;
+                    const CUtensorMap* ma = &args.maps[second ? p.a1 : p.a0];
+                    const CUtensorMap* mb = &args.maps[second ? p.b1 : p.b0];
+                    if (EPI == kGatedForward) mb += rank;
+                    const int k = (second ? kt - p.k0 : kt) * 64;
+                    uint8_t* dst = smem + stage * kStageBytes;
+                    const uint32_t bar = full0 + static_cast<uint32_t>(stage) * 8u;
+                    if (leader) mbar_arrive_expect_tx(&full[stage], 2u * kStageBytes);
+                    load_operand(dst, ma, bar, a_mn, k, row0);
+                    load_operand(dst + kOperandBytes, mb, bar, b_mn, k, col0);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // every stage this CTA filled has been released, so no commit
+            // arrival is still on its way to this CTA
+            for (int i = 0; i < kStages && ok; ++i) {
+                if (!mbar_wait(&empty[stage], phase ^ 1u, err)) break;
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (leader) {
+            // The whole warp runs the loop and one elected lane issues (see
+            // gemm.cu, where this form measured 2-4% faster than one lane).
+            // Stage s adds s * kStageBytes / 16 to a descriptor's address
+            // field.  Within a stage an MMA's 16 K values are 32 bytes of a
+            // K-major row, or 16 rows of 128 bytes of an MN-major box.
+            const uint32_t smem0 = smem_u32(smem);
+            constexpr uint64_t kStageStep = kStageBytes >> 4;
+            int stage = 0;
+            uint32_t phase = 0;
+            uint64_t off = 0;
+            bool ok = true;
+            int local = 0;
+            for (int u = pair; ok && unit_at(u, args, w); u += num_pairs, ++local) {
+                const Problem& p = args.p[w.problem];
+                const bool a_mn = p.a_mn, b_mn = p.b_mn;
+                const uint32_t idesc = make_idesc_bf16(kTile, kTile, false) | (a_mn ? 1u << 15 : 0u) |
+                                       (b_mn ? 1u << 16 : 0u);
+                // MN-major: 64-value blocks 8 KB apart, groups of eight K rows 1 KB apart
+                const uint64_t desc_a = make_sdesc(smem0, a_mn ? kOperandBytes / 2 : 16, 1024, kSw128);
+                const uint64_t desc_b = make_sdesc(smem0 + kOperandBytes, b_mn ? kOperandBytes / 2 : 16, 1024, kSw128);
+                const uint64_t step_a = a_mn ? 128 : 2, step_b = b_mn ? 128 : 2;
+                const int buf = local & 1;
+                const uint32_t use = static_cast<uint32_t>(local >> 1);
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_empty[buf], (use & 1u) ^ 1u, err))) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(buf * kTile);
+                for (int kt = w.kb; kt < w.ke; ++kt) {
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, err))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t a = desc_a + off, b = desc_b + off;
+                    if (elect_one()) {
+                        mma_f16_pair(d, a, b, idesc, kt != w.kb);
+                        mma_f16_pair(d, a + step_a, b + step_b, idesc, 1u);
+                        mma_f16_pair(d, a + 2 * step_a, b + 2 * step_b, idesc, 1u);
+                        mma_f16_pair(d, a + 3 * step_a, b + 3 * step_b, idesc, 1u);
+                        tc_commit_pair_mc(&empty[stage], 0x3);
+                    }
+                    off += kStageStep;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        off = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (elect_one()) tc_commit_pair_mc(&acc_full[buf], 0x3);
+            }
+            // every MMA of the pair has finished before tensor memory is freed
+            if (elect_one()) tc_commit_pair_mc(done_bar, 0x1);
+            mbar_wait(done_bar, 0, nullptr);
+        }
+        __syncwarp();
+    } else {
+        const int quad = warp & 3;          // tensor-memory lane quadrant of this warp
+        const int part = (warp - 2) >> 2;   // which share of the columns
+        const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+        int local = 0;
+        for (int u = pair; unit_at(u, args, w); u += num_pairs, ++local) {
+            const Problem& p = args.p[w.problem];
+            const int buf = local & 1;
+            const uint32_t use = static_cast<uint32_t>(local >> 1);
+            const int row_in_cta = quad * 32 + lane;
+            const int row = w.mp * kTile + static_cast<int>(rank) * kHalf + row_in_cta;
+            const bool row_ok = row < p.rows;
+            const size_t row_at = static_cast<size_t>(row) * p.cols;
+            const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * kTile) + lane_addr;
+            if (!whole_warp_wait(&acc_full[buf], use & 1u, err)) break;
+            tc_fence_after();
+            if constexpr (EPI == kGatedForward) {
+                constexpr int kCols = kHalf / (kEpiWarps / 4);
+                const int c0 = part * kCols;
+#pragma unroll 1
+                for (int c = c0; c < c0 + kCols; c += 32) {
+                    uint32_t g[32], v[32];
+                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), g);
+                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(kHalf + c), v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int col = w.nt * kHalf + c + 8 * q;
+                        float gf[8], uf[8], hf[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            gf[j] = __uint_as_float(g[8 * q + j]);
+                            uf[j] = __uint_as_float(v[8 * q + j]);
+                            hf[j] = act_value<ACT>(gf[j]) * uf[j];
+                        }
+                        if (row_ok && col < p.cols) {
+                            *reinterpret_cast<uint4*>(p.out[0] + row_at + col) = pack8(hf);
+                            if (p.out[1]) {
+                                *reinterpret_cast<uint4*>(p.out[1] + row_at + col) = pack8(gf);
+                                *reinterpret_cast<uint4*>(p.out[2] + row_at + col) = pack8(uf);
+                            }
+                        }
+                    }
+                }
+            } else if constexpr (EPI == kGatedBackward) {
+                constexpr int kCols = kTile / (kEpiWarps / 4);
+                const int c0 = part * kCols;
+#pragma unroll 1
+                for (int c = c0; c < c0 + kCols; c += 32) {
+                    uint32_t r[32];
+                    uint4 gp[4], up[4];
+                    const int col0 = w.nt * kTile + c;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        gp[q] = up[q] = make_uint4(0, 0, 0, 0);
+                        if (row_ok && col0 + 8 * q < p.cols) {
+                            gp[q] = __ldg(reinterpret_cast<const uint4*>(p.in[0] + row_at + col0 + 8 * q));
+                            up[q] = __ldg(reinterpret_cast<const uint4*>(p.in[1] + row_at + col0 + 8 * q));
+                        }
+                    }
+                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float gf[8], uf[8];
+                        unpack8(gp[q], gf);
+                        unpack8(up[q], uf);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float dh = __uint_as_float(r[8 * q + j]);
+                            float value, slope;
+                            act_both<ACT>(gf[j], value, slope);
+                            gf[j] = dh * uf[j] * slope;
+                            uf[j] = dh * value;
+                        }
+                        if (row_ok && col0 + 8 * q < p.cols) {
+                            *reinterpret_cast<uint4*>(p.out[0] + row_at + col0 + 8 * q) = pack8(gf);
+                            *reinterpret_cast<uint4*>(p.out[1] + row_at + col0 + 8 * q) = pack8(uf);
+                        }
+                    }
+                }
+            } else if (p.split > 1) {
+                // this CTA's half of the fp32 partial: [column / 4][row][4]
+                float* dst = p.part + (static_cast<size_t>(u - p.first_unit) * 2 + rank) * (kHalf * kTile);
+#pragma unroll 1
+                for (int c = 0; c < kTile; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        reinterpret_cast<uint4*>(dst)[(c / 4 + q) * kHalf + row_in_cta] =
+                            make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < kTile; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), r);
+                    tmem_ld_wait();
+                    const int col0 = w.nt * kTile + c;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float f[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[8 * q + j]);
+                        if (row_ok && col0 + 8 * q < p.cols)
+                            *reinterpret_cast<uint4*>(p.out[0] + row_at + col0 + 8 * q) = pack8(f);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+        }
+    }
+
+    __syncwarp();  // reconverge the role warps before the cluster barrier
+    // after an abort, copies still in flight get time to land before the
+    // shared memory they target is released
+    if (error_seen(err)) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+    }
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, kTmemColumns);
+    }
+}
+
+// Sums the partial tiles of a split problem in part order and rounds: a
+// thread owns eight columns of one row.  Grid: (tile * 2 + rank) x 16, with
+// 256 threads = 2 column octets x 128 rows.
+__global__ void __launch_bounds__(256) rtlynx_gated_sum_parts_kernel(const __grid_constant__ Problem p) {
+    grid_dependency_wait();
+    const int tile = blockIdx.x >> 1, rank = blockIdx.x & 1;
+    const int row_in_cta = threadIdx.x & 127, octet = blockIdx.y * 2 + (threadIdx.x >> 7);
+    const int per_group = p.m_pairs * p.group_n;
+    const int g = tile / per_group;
+    const int width = min(p.group_n, p.n_tiles - g * p.group_n);
+    const int in_group = tile - g * per_group;
+    const int row = (in_group / width) * kTile + rank * kHalf + row_in_cta;
+    const int col = (g * p.group_n + in_group % width) * kTile + 8 * octet;
+    if (row >= p.rows || col >= p.cols) return;
+    float sum[8] = {};
+    for (int s = 0; s < p.split; ++s) {
+        const float4* src = reinterpret_cast<const float4*>(
+            p.part + ((static_cast<size_t>(tile) * p.split + s) * 2 + rank) * (kHalf * kTile));
+        const float4 a = src[(2 * octet) * kHalf + row_in_cta], b = src[(2 * octet + 1) * kHalf + row_in_cta];
+        sum[0] += a.x, sum[1] += a.y, sum[2] += a.z, sum[3] += a.w;
+        sum[4] += b.x, sum[5] += b.y, sum[6] += b.z, sum[7] += b.w;
+    }
+    *reinterpret_cast<uint4*>(p.out[0] + static_cast<size_t>(row) * p.cols + col) = pack8(sum);
+}
+
+// ---------------------------------------------------------------- host side
+template <int EPI, int ACT>
+int launch_gated(const GatedArgs& args, int num_sms, cudaStream_t stream) {
+    auto kernel = rtlynx_gated_gemm_kernel<EPI, ACT>;
+    static std::atomic<uint64_t> smem_set{0};
+    const int e = allow_max_dynamic_smem(kernel, smem_set);
+    if (e) return e;
+    const int most = num_sms / 2;
+    const int pairs = args.units < most ? args.units : most;
+    return launch_dependent(kernel, dim3(2 * pairs), dim3(Shape<EPI>::kThreads), kSmemBytes, stream, args);
+}
+
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+// Column tiles swept together: one while both operands stay in L2, else as
+// many as 48 MiB of B hold (the linear layer's rule, gemm.cu).
+int raster_group(const Problem& p, int64_t k_values) {
+    const double a = static_cast<double>(p.m_pairs) * kTile * k_values * 2.0;
+    const double tile = static_cast<double>(kTile) * k_values * 2.0, b = tile * p.n_tiles;
+    if (a + b <= 192.0 * (1 << 20)) return 1;
+    const int n = static_cast<int>(48.0 * (1 << 20) / tile);
+    return n < 1 ? 1 : (n > p.n_tiles ? p.n_tiles : n);
+}
+
+struct Maps {
+    GatedArgs& args;
+    int count = 0;
+    bool ok = true;
+    // a [rows, cols] bf16 matrix read in boxes of 64 contiguous values x box_rows
+    int add(const void* base, int64_t rows, int64_t cols, bool mn) {
+        if (encode_tmap_uncached(&args.maps[count], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, cols * 2, 64,
+                                 mn ? 64 : kHalf, CU_TENSOR_MAP_SWIZZLE_128B))
+            ok = false;
+        return count++;
+    }
+};
+
+int check_sizes(int64_t M, int64_t D, int64_t F, int act) {
+    if (M <= 0 || D <= 0 || F <= 0 || D % 8 || F % 8) return RTLYNX_ERR_INVALID_ARG;
+    if (act != RTLYNX_ACT_SILU && act != RTLYNX_ACT_GELU) return RTLYNX_ERR_INVALID_ARG;
+    // tile counts and tensor-map coordinates fit 32 bits with room
+    if (M > (int64_t(1) << 28) || D > (int64_t(1) << 22) || F > (int64_t(1) << 22)) return RTLYNX_ERR_UNSUPPORTED;
+    if (M / kTile * (F / kHalf) > (int64_t(1) << 28) || M / kTile * (D / kHalf) > (int64_t(1) << 28))
+        return RTLYNX_ERR_UNSUPPORTED;
+    return RTLYNX_OK;
+}
+
+struct Range {
+    const void* p;
+    uint64_t bytes;
+};
+
+// Every output range is given, 16-byte aligned, and shares no byte with an
+// input or another output (null ones aside).
+bool ranges_ok(const Range* in, int n_in, const Range* out, int n_out) {
+    auto meet = [](const Range& a, const Range& b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+    };
+    auto aligned = [](const Range& a) { return (reinterpret_cast<uintptr_t>(a.p) & 15u) == 0; };
+    for (int i = 0; i < n_in; ++i)
+        if (!aligned(in[i])) return false;
+    for (int i = 0; i < n_out; ++i) {
+        if (!aligned(out[i])) return false;
+        for (int j = 0; j < n_in; ++j)
+            if (meet(out[i], in[j])) return false;
+        for (int j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return false;
+    }
+    return true;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// dX's tiles are few and long (K = 2 D_ff) when there are few tokens: they are
+// cut along K until the launch has a part for every CTA pair, at least eight
+// stages each.
+int dx_split(int64_t M, int64_t D, int64_t F, int pairs) {
+    const int64_t tiles = static_cast<int64_t>(ceil_div(M, kTile)) * ceil_div(D, kTile);
+    const int64_t stages = 2 * ceil_div(F, 64);
+    int64_t split = pairs / tiles;
+    if (split > stages / 8) split = stages / 8;
+    return static_cast<int>(split < 1 ? 1 : (split > 16 ? 16 : split));
+}
+
+constexpr int kAssumedPairs = 74;  // sizes the workspace; a GPU with fewer pairs splits less
+
+struct BackwardLayout {
+    size_t dg, du, part, total;
+};
+
+BackwardLayout backward_layout(int64_t M, int64_t D, int64_t F) {
+    BackwardLayout l;
+    l.dg = 0;
+    l.du = align256(static_cast<size_t>(M) * F * 2);
+    l.part = 2 * l.du;
+    const int split = dx_split(M, D, F, kAssumedPairs);
+    const size_t units = static_cast<size_t>(ceil_div(M, kTile)) * ceil_div(D, kTile) * split;
+    l.total = l.part + (split > 1 ? units * kTile * kTile * sizeof(float) : 0);
+    return l;
+}
+
+}  // namespace
+}  // namespace rtlynx
+
+using namespace rtlynx;
+
+extern "C" {
+
+int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, const void* W_down,
+                           const void* LA_down, const void* LB_down, void* G, void* U, void* H, void* Y, int64_t M,
+                           int64_t D, int64_t D_ff, int64_t R, int act, int mode_down, void* stream_) {
+    int rc = check_sizes(M, D, D_ff, act);
+    if (rc) return rc;
+    if (!X || !W_gate || !W_up || !W_down || !H || !Y || (G == nullptr) != (U == nullptr))
+        return RTLYNX_ERR_INVALID_ARG;
+    rc = validate(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down);
+    if (rc) return rc;
+    const uint64_t x_bytes = 2ull * M * D, h_bytes = 2ull * M * D_ff, w_bytes = 2ull * D * D_ff;
+    const bool lora = mode_down == RTLYNX_MODE_SPARSE && R > 0;
+    const Range in[6] = {{X, x_bytes},
+                         {W_gate, w_bytes},
+                         {W_up, w_bytes},
+                         {W_down, w_bytes},
+                         {lora ? LA_down : nullptr, 2ull * D * (lora ? R : 0)},
+                         {lora ? LB_down : nullptr, 2ull * D_ff * (lora ? R : 0)}};
+    const Range out[4] = {{H, h_bytes}, {Y, x_bytes}, {G, h_bytes}, {U, h_bytes}};
+    if (!ranges_ok(in, 6, out, 4)) return RTLYNX_ERR_INVALID_ARG;
+    int num_sms = 0;
+    int* err = nullptr;
+    rc = device_info(&num_sms, &err);
+    if (rc) return rc;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+
+    GatedArgs args{};
+    Maps maps{args};
+    args.problems = 1;
+    args.act = act;
+    args.err = err;
+    Problem& p = args.p[0];
+    p.m_pairs = ceil_div(M, kTile);
+    p.n_tiles = ceil_div(D_ff, kHalf);
+    p.split = 1;
+    p.k0 = p.k = ceil_div(D, 64);
+    p.a0 = p.a1 = maps.add(X, M, D, false);
+    p.b0 = p.b1 = maps.add(W_gate, D_ff, D, false);
+    maps.add(W_up, D_ff, D, false);
+    if (!maps.ok) return RTLYNX_ERR_CUDA;
+    p.group_n = raster_group(p, D);
+    p.rows = static_cast<int>(M);
+    p.cols = static_cast<int>(D_ff);
+    p.out[0] = static_cast<uint16_t*>(H);
+    p.out[1] = static_cast<uint16_t*>(G);
+    p.out[2] = static_cast<uint16_t*>(U);
+    args.units = p.m_pairs * p.n_tiles;
+    const int e = act == RTLYNX_ACT_SILU ? launch_gated<kGatedForward, RTLYNX_ACT_SILU>(args, num_sms, stream)
+                                         : launch_gated<kGatedForward, RTLYNX_ACT_GELU>(args, num_sms, stream);
+    if (e) return RTLYNX_ERR_CUDA;
+    return rtlynx_linear(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down, stream_);
+}
+
+size_t rtlynx_gated_mlp_backward_workspace_size(int64_t M, int64_t D, int64_t D_ff) {
+    if (check_sizes(M, D, D_ff, RTLYNX_ACT_SILU)) return 0;
+    return backward_layout(M, D, D_ff).total;
+}
+
+int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate, const void* W_up, const void* W_down,
+                              const void* G, const void* U, const void* H, void* dX, void* dW_gate, void* dW_up,
+                              void* dW_down, int64_t M, int64_t D, int64_t D_ff, int act, void* workspace,
+                              size_t ws_bytes, void* stream_) {
+    int rc = check_sizes(M, D, D_ff, act);
+    if (rc) return rc;
+    if (!dY || !X || !W_gate || !W_up || !W_down || !G || !U || !H || !workspace) return RTLYNX_ERR_INVALID_ARG;
+    const BackwardLayout l = backward_layout(M, D, D_ff);
+    if (ws_bytes < l.total || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return RTLYNX_ERR_INVALID_ARG;
+    const uint64_t x_bytes = 2ull * M * D, h_bytes = 2ull * M * D_ff, w_bytes = 2ull * D * D_ff;
+    const Range in[8] = {{dY, x_bytes},     {X, x_bytes}, {W_gate, w_bytes}, {W_up, w_bytes},
+                         {W_down, w_bytes}, {G, h_bytes}, {U, h_bytes},      {H, h_bytes}};
+    const Range out[5] = {{dX, x_bytes}, {dW_gate, w_bytes}, {dW_up, w_bytes}, {dW_down, w_bytes}, {workspace, l.total}};
+    if (!ranges_ok(in, 8, out, 5)) return RTLYNX_ERR_INVALID_ARG;
+    if (!dX && !dW_gate && !dW_up && !dW_down) return RTLYNX_OK;
+    int num_sms = 0;
+    int* err = nullptr;
+    rc = device_info(&num_sms, &err);
+    if (rc) return rc;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    uint16_t* dG = reinterpret_cast<uint16_t*>(base + l.dg);
+    uint16_t* dU = reinterpret_cast<uint16_t*>(base + l.du);
+
+    const int m_pairs = ceil_div(M, kTile), token_stages = ceil_div(M, 64);
+    if (dX || dW_gate || dW_up) {
+        // dH = dY Wd, taken to dG and dU before it leaves the chip
+        GatedArgs args{};
+        Maps maps{args};
+        args.problems = 1;
+        args.act = act;
+        args.err = err;
+        Problem& p = args.p[0];
+        p.m_pairs = m_pairs;
+        p.n_tiles = ceil_div(D_ff, kTile);
+        p.split = 1;
+        p.k0 = p.k = ceil_div(D, 64);
+        p.a0 = p.a1 = maps.add(dY, M, D, false);
+        p.b0 = p.b1 = maps.add(W_down, D, D_ff, true);
+        p.b_mn = 1;
+        if (!maps.ok) return RTLYNX_ERR_CUDA;
+        p.group_n = raster_group(p, D);
+        p.rows = static_cast<int>(M);
+        p.cols = static_cast<int>(D_ff);
+        p.out[0] = dG;
+        p.out[1] = dU;
+        p.in[0] = static_cast<const uint16_t*>(G);
+        p.in[1] = static_cast<const uint16_t*>(U);
+        args.units = p.m_pairs * p.n_tiles;
+        const int e = act == RTLYNX_ACT_SILU ? launch_gated<kGatedBackward, RTLYNX_ACT_SILU>(args, num_sms, stream)
+                                             : launch_gated<kGatedBackward, RTLYNX_ACT_GELU>(args, num_sms, stream);
+        if (e) return RTLYNX_ERR_CUDA;
+    }
+
+    GatedArgs args{};
+    Maps maps{args};
+    args.act = act;
+    args.err = err;
+    int dx_index = -1;
+    auto close = [&](Problem& p, int64_t rows, int64_t cols, void* out, int64_t k_values) {
+        p.m_pairs = ceil_div(rows, kTile);
+        p.n_tiles = ceil_div(cols, kTile);
+        p.rows = static_cast<int>(rows);
+        p.cols = static_cast<int>(cols);
+        p.out[0] = static_cast<uint16_t*>(out);
+        p.group_n = raster_group(p, k_values);
+        p.first_unit = args.units;
+        args.units += p.m_pairs * p.n_tiles * p.split;
+        ++args.problems;
+    };
+    if (dX) {
+        Problem& p = args.p[args.problems];
+        dx_index = args.problems;
+        p.k0 = ceil_div(D_ff, 64);
+        p.k = 2 * p.k0;
+        p.a0 = maps.add(dG, M, D_ff, false);
+        p.b0 = maps.add(W_gate, D_ff, D, true);
+        p.a1 = maps.add(dU, M, D_ff, false);
+        p.b1 = maps.add(W_up, D_ff, D, true);
+        p.b_mn = 1;
+        p.split = dx_split(M, D, D_ff, num_sms / 2 < kAssumedPairs ? num_sms / 2 : kAssumedPairs);
+        p.part = reinterpret_cast<float*>(base + l.part);
+        close(p, M, D, dX, 2 * D_ff);
+    }
+    auto weight_grad = [&](const void* a, int64_t a_cols, const void* b, int64_t b_cols, void* out) {
+        Problem& p = args.p[args.problems];
+        p.k0 = p.k = token_stages;
+        p.a0 = p.a1 = maps.add(a, M, a_cols, true);
+        p.b0 = p.b1 = maps.add(b, M, b_cols, true);
+        p.a_mn = p.b_mn = 1;
+        p.split = 1;
+        close(p, a_cols, b_cols, out, M);
+    };
+    if (dW_gate) weight_grad(dG, D_ff, X, D, dW_gate);
+    if (dW_up) weight_grad(dU, D_ff, X, D, dW_up);
+    if (dW_down) weight_grad(dY, D, H, D_ff, dW_down);
+    if (!maps.ok) return RTLYNX_ERR_CUDA;
+    if (launch_gated<kStore, 0>(args, num_sms, stream)) return RTLYNX_ERR_CUDA;
+    if (dx_index >= 0 && args.p[dx_index].split > 1) {
+        const Problem& p = args.p[dx_index];
+        if (launch_dependent(rtlynx_gated_sum_parts_kernel, dim3(p.m_pairs * p.n_tiles * 2, 16), dim3(256), 0, stream, p))
+            return RTLYNX_ERR_CUDA;
+    }
+    return RTLYNX_OK;
+}
+
+}  // extern "C"

@@ -196,6 +196,45 @@ int rtlynx_mlp_block(const void* X, const void* W_up, const void* LA_up, const v
                      const void* LA_down, const void* LB_down, void* H, void* Y, int64_t M, int64_t D, int64_t D_ff,
                      int64_t R, int mode_up, int mode_down, void* stream);
 
+/*
+ * rtlynx_gated_mlp_block - a gated feed-forward block (SwiGLU, GeGLU):
+ *   G = X W_gate^T, U = X W_up^T, H = act(G) * U   [M, D_ff], one kernel
+ *   Y = layer_down(H)                              [M, D]
+ *   act      rtlynx_act: SiLU, x / (1 + exp(-x)), or GELU in its erf form
+ *   layer_down runs as rtlynx_linear with mode_down and its LoRA pair
+ *   (RTLYNX_MODE_DENSE_SKIP: Y = H W_down^T)
+ *   X [M, D], W_gate, W_up [D_ff, D], W_down [D, D_ff], LA_down [D, R],
+ *   LB_down [R, D_ff], all bf16, device; D and D_ff multiples of 8.
+ *   H  caller-owned [M, D_ff] bf16 buffer that receives act(G) * U
+ *   G, U  caller-owned [M, D_ff] bf16 buffers that receive the projections, for
+ *      rtlynx_gated_mlp_backward; both NULL where no gradient follows
+ * The projections are accumulated in 32 bits; H is made from them before they
+ * are rounded.  Outputs may not share a byte with an input or one another.
+ * M > 2^28, D or D_ff > 2^22 give RTLYNX_ERR_UNSUPPORTED.
+ */
+typedef enum { RTLYNX_ACT_SILU = 0, RTLYNX_ACT_GELU = 1 } rtlynx_act;
+
+int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, const void* W_down,
+                           const void* LA_down, const void* LB_down, void* G, void* U, void* H, void* Y, int64_t M,
+                           int64_t D, int64_t D_ff, int64_t R, int act, int mode_down, void* stream);
+
+/* Gradients of the block with a dense down-projection (mode_down =
+ * RTLYNX_MODE_DENSE_SKIP), from dY [M, D] and what the forward call wrote:
+ *   dH = dY W_down, dG = dH * U * act'(G), dU = dH * act(G)
+ *   dX = dG W_gate + dU W_up, dW_gate = dG^T X, dW_up = dU^T X, dW_down = dY^T H
+ * dX and each weight's gradient [bf16, shape of what it belongs to] may be
+ * NULL: it is then not computed (none at all: nothing is launched).  Sums are
+ * held in 32 bits in a fixed order; dG and dU are rounded to bf16 between the
+ * products.  workspace: rtlynx_gated_mlp_backward_workspace_size(M, D, D_ff)
+ * bytes (0 for invalid sizes) of device memory, 256-byte aligned, for this
+ * call until it has finished. */
+size_t rtlynx_gated_mlp_backward_workspace_size(int64_t M, int64_t D, int64_t D_ff);
+
+int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate, const void* W_up, const void* W_down,
+                              const void* G, const void* U, const void* H, void* dX, void* dW_gate, void* dW_up,
+                              void* dW_down, int64_t M, int64_t D, int64_t D_ff, int act, void* workspace,
+                              size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- query and key heads
  * What stands between the qkv layer and attention in a transformer block:
  * rotary positions with several axes (time, height and width of a video
