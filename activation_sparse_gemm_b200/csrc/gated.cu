@@ -34,6 +34,8 @@
 #include "internal.h"
 #include "ptx.cuh"
 
+#include <type_traits>
+
 namespace rtlynx {
 namespace {
 
@@ -102,15 +104,26 @@ __device__ __forceinline__ bool whole_warp_wait(uint64_t* bar, uint32_t parity, 
     return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
 }
 
+using KMajor = std::integral_constant<bool, false>;
+using MnMajor = std::integral_constant<bool, true>;
+
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
 // 128 x 64 values into shared memory, 128B swizzle.  K-major: 128 rows of 64
 // K values.  MN-major: two boxes of 64 row values x 64 K.
-__device__ __forceinline__ void load_operand(uint8_t* dst, const CUtensorMap* map, uint32_t bar, bool mn, int k,
-                                             int row) {
-    if (mn) {
-        tma_load_2d_pair(dst, map, bar, row, k);
-        tma_load_2d_pair(dst + kOperandBytes / 2, map, bar, row + 64, k);
+template <bool MN>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, uint32_t bar, int k, int row) {
+    if (MN) {
+        tma_load_pair(dst, map, bar, row, k);
+        tma_load_pair(dst + kOperandBytes / 2, map, bar, row + 64, k);
     } else {
-        tma_load_2d_pair(dst, map, bar, k, row);
+        tma_load_pair(dst, map, bar, k, row);
     }
 }
 
@@ -184,47 +197,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
 
     Unit w;
     if (warp == 0) {
-        if (lane == 0) {
-            const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int u = pair; ok && unit_at(u, args, w); u += num_pairs) {
-                const Problem& p = args.p[w.problem];
-                const int row0 = w.mp * kTile + static_cast<int>(rank) * kHalf;
-                const int col0 = EPI == kGatedForward ? w.nt * kHalf : w.nt * kTile + static_cast<int>(rank) * kHalf;
-                const bool a_mn = p.a_mn, b_mn = p.b_mn;
-                for (int kt = w.kb; kt < w.ke; ++kt) {
-                    if (!mbar_wait(&empty[stage], phase ^ 1u, err)) {
-                        ok = false;
-                        break;
-                    }
-                    const bool second = kt >= p.k0;
-                    const CUtensorMap* ma = &args.maps[second ? p.a1 : p.a0];
-                    const CUtensorMap* mb = &args.maps[second ? p.b1 : p.b0];
-                    if (EPI == kGatedForward) mb += rank;
-                    const int k = (second ? kt - p.k0 : kt) * 64;
-                    uint8_t* dst = smem + stage * kStageBytes;
-                    const uint32_t bar = full0 + static_cast<uint32_t>(stage) * 8u;
-                    if (leader) mbar_arrive_expect_tx(&full[stage], 2u * kStageBytes);
-                    load_operand(dst, ma, bar, a_mn, k, row0);
-                    load_operand(dst + kOperandBytes, mb, bar, b_mn, k, col0);
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+        // The whole warp runs the loop and one elected lane issues, so that
+        // addresses, coordinates and map pointers are uniform values: the two
+        // to four loads of a stage have to be issued in the 256 cycles that
+        // its MMAs take.
+        const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
+        const uint32_t smem0 = smem_u32(smem);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        auto fetch = [&](auto a_major, auto b_major, const CUtensorMap* ma, const CUtensorMap* mb, int k, int stages,
+                         int row0, int col0) {
+            constexpr bool A_MN = decltype(a_major)::value, B_MN = decltype(b_major)::value;
+            for (int i = 0; i < stages; ++i, k += 64) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], phase ^ 1u, err))) {
+                    ok = false;
+                    break;
                 }
-            }
-            // every stage this CTA filled has been released, so no commit
-            // arrival is still on its way to this CTA
-            for (int i = 0; i < kStages && ok; ++i) {
-                if (!mbar_wait(&empty[stage], phase ^ 1u, err)) break;
+                const uint32_t dst = smem0 + static_cast<uint32_t>(stage * kStageBytes);
+                const uint32_t bar = full0 + static_cast<uint32_t>(stage) * 8u;
+                if (elect_one()) {
+                    if (leader) mbar_arrive_expect_tx(&full[stage], 2u * kStageBytes);
+                    load_operand<A_MN>(dst, ma, bar, k, row0);
+                    load_operand<B_MN>(dst + kOperandBytes, mb, bar, k, col0);
+                }
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
+        };
+        for (int u = pair; ok && unit_at(u, args, w); u += num_pairs) {
+            const Problem& p = args.p[w.problem];
+            const int row0 = w.mp * kTile + static_cast<int>(rank) * kHalf;
+            const int col0 = EPI == kGatedForward ? w.nt * kHalf : w.nt * kTile + static_cast<int>(rank) * kHalf;
+            // one run of stages for each operand pair
+            for (int seg = 0; seg < 2 && ok; ++seg) {
+                const int begin = seg ? max(w.kb, p.k0) : w.kb, end = seg ? w.ke : min(w.ke, p.k0);
+                const CUtensorMap* ma = &args.maps[seg ? p.a1 : p.a0];
+                const CUtensorMap* mb = &args.maps[(seg ? p.b1 : p.b0) + (EPI == kGatedForward ? static_cast<int>(rank) : 0)];
+                const int k = (begin - (seg ? p.k0 : 0)) * 64;
+                if (EPI == kGatedForward) {
+                    fetch(KMajor(), KMajor(), ma, mb, k, end - begin, row0, col0);
+                } else if (EPI == kGatedBackward || !p.a_mn) {
+                    fetch(KMajor(), MnMajor(), ma, mb, k, end - begin, row0, col0);
+                } else {
+                    fetch(MnMajor(), MnMajor(), ma, mb, k, end - begin, row0, col0);
+                }
+            }
         }
+        // every stage this CTA filled has been released, so no commit arrival
+        // is still on its way to this CTA
+        for (int i = 0; i < kStages && ok; ++i) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], phase ^ 1u, err))) break;
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        __syncwarp();
     } else if (warp == 1) {
         if (leader) {
             // The whole warp runs the loop and one elected lane issues (see
@@ -233,46 +264,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
             // field.  Within a stage an MMA's 16 K values are 32 bytes of a
             // K-major row, or 16 rows of 128 bytes of an MN-major box.
             const uint32_t smem0 = smem_u32(smem);
-            constexpr uint64_t kStageStep = kStageBytes >> 4;
             int stage = 0;
             uint32_t phase = 0;
             uint64_t off = 0;
             bool ok = true;
             int local = 0;
-            for (int u = pair; ok && unit_at(u, args, w); u += num_pairs, ++local) {
-                const Problem& p = args.p[w.problem];
-                const bool a_mn = p.a_mn, b_mn = p.b_mn;
-                const uint32_t idesc = make_idesc_bf16(kTile, kTile, false) | (a_mn ? 1u << 15 : 0u) |
-                                       (b_mn ? 1u << 16 : 0u);
+            // the stages of one unit, operand layouts fixed at compile time so
+            // that descriptors, steps and the instruction word stay constants
+            // and uniform values
+            auto issue = [&](auto a_major, auto b_major, uint32_t d, int stages) {
+                constexpr bool A_MN = decltype(a_major)::value, B_MN = decltype(b_major)::value;
+                constexpr uint32_t idesc = make_idesc_bf16(kTile, kTile, false) | (A_MN ? 1u << 15 : 0u) |
+                                           (B_MN ? 1u << 16 : 0u);
                 // MN-major: 64-value blocks 8 KB apart, groups of eight K rows 1 KB apart
-                const uint64_t desc_a = make_sdesc(smem0, a_mn ? kOperandBytes / 2 : 16, 1024, kSw128);
-                const uint64_t desc_b = make_sdesc(smem0 + kOperandBytes, b_mn ? kOperandBytes / 2 : 16, 1024, kSw128);
-                const uint64_t step_a = a_mn ? 128 : 2, step_b = b_mn ? 128 : 2;
-                const int buf = local & 1;
-                const uint32_t use = static_cast<uint32_t>(local >> 1);
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_empty[buf], (use & 1u) ^ 1u, err))) break;
-                tc_fence_after();
-                const uint32_t d = tmem_base + static_cast<uint32_t>(buf * kTile);
-                for (int kt = w.kb; kt < w.ke; ++kt) {
+                const uint64_t desc_a = make_sdesc(smem0, A_MN ? kOperandBytes / 2 : 16, 1024, kSw128);
+                const uint64_t desc_b = make_sdesc(smem0 + kOperandBytes, B_MN ? kOperandBytes / 2 : 16, 1024, kSw128);
+                constexpr uint64_t step_a = A_MN ? 128 : 2, step_b = B_MN ? 128 : 2;
+                constexpr uint64_t kStageStep = kStageBytes >> 4;
+                for (int i = 0; i < stages; ++i) {
                     if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, err))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint64_t a = desc_a + off, b = desc_b + off;
+                    const uint32_t acc = i != 0;
                     if (elect_one()) {
-                        mma_f16_pair(d, a, b, idesc, kt != w.kb);
+                        mma_f16_pair(d, a, b, idesc, acc);
                         mma_f16_pair(d, a + step_a, b + step_b, idesc, 1u);
                         mma_f16_pair(d, a + 2 * step_a, b + 2 * step_b, idesc, 1u);
                         mma_f16_pair(d, a + 3 * step_a, b + 3 * step_b, idesc, 1u);
-                        tc_commit_pair_mc(&empty[stage], 0x3);
                     }
+                    if (elect_one()) tc_commit_pair_mc(&empty[stage], 0x3);
                     off += kStageStep;
                     if (++stage == kStages) {
                         stage = 0;
                         off = 0;
                         phase ^= 1u;
                     }
+                }
+            };
+            for (int u = pair; ok && unit_at(u, args, w); u += num_pairs, ++local) {
+                const Problem& p = args.p[w.problem];
+                const int buf = local & 1;
+                const uint32_t use = static_cast<uint32_t>(local >> 1);
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_empty[buf], (use & 1u) ^ 1u, err))) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(buf * kTile);
+                if (EPI == kGatedForward) {
+                    issue(KMajor(), KMajor(), d, w.ke - w.kb);
+                } else if (EPI == kGatedBackward || !p.a_mn) {
+                    issue(KMajor(), MnMajor(), d, w.ke - w.kb);
+                } else {
+                    issue(MnMajor(), MnMajor(), d, w.ke - w.kb);
                 }
                 if (!ok) break;
                 if (elect_one()) tc_commit_pair_mc(&acc_full[buf], 0x3);
