@@ -69,23 +69,42 @@ struct GatedArgs {
     CUtensorMap maps[kMaxMaps];
     Problem p[kMaxProblems];
     int problems, units;
-    int act;
+    int longs, extra;  // see unit_at
     int* err;
 };
 
 struct Unit {
     int problem, mp, nt, kb, ke, part;
+    int index;  // among the problem's units
 };
 
-__device__ __forceinline__ bool unit_at(int u, const GatedArgs& args, Unit& w) {
+// Unit i of a CTA pair.  The first `longs` units (dX, whose K is 2 D_ff) are
+// dealt round; the pairs from `rest` on, which have one of them less, take
+// `extra` of the others each instead, and what is left is dealt round.
+__device__ __forceinline__ bool unit_at(int i, int pair, int pairs, const GatedArgs& args, Unit& w) {
+    const int rest = args.longs % pairs;
+    const int own = args.longs / pairs + (pair < rest ? 1 : 0);
+    int u;
+    if (i < own) {
+        u = pair + i * pairs;
+    } else {
+        int j = i - own;
+        if (pair >= rest && j < args.extra) {
+            u = j * (pairs - rest) + pair - rest;
+        } else {
+            if (pair >= rest) j -= args.extra;
+            u = args.extra * (pairs - rest) + j * pairs + pair;
+        }
+        u += args.longs;
+    }
     if (u >= args.units) return false;
-    int i = 0;
-    while (i + 1 < args.problems && u >= args.p[i + 1].first_unit) ++i;
-    const Problem& p = args.p[i];
-    const int local = u - p.first_unit;
-    const int tile = local / p.split;
-    w.problem = i;
-    w.part = local - tile * p.split;
+    int n = 0;
+    while (n + 1 < args.problems && u >= args.p[n + 1].first_unit) ++n;
+    const Problem& p = args.p[n];
+    w.index = u - p.first_unit;
+    const int tile = w.index / p.split;
+    w.problem = n;
+    w.part = w.index - tile * p.split;
     w.kb = static_cast<int>(static_cast<int64_t>(w.part) * p.k / p.split);
     w.ke = static_cast<int>(static_cast<int64_t>(w.part + 1) * p.k / p.split);
     // column tiles in groups of group_n, a group's tiles row pair by row pair
@@ -227,7 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
                 }
             }
         };
-        for (int u = pair; ok && unit_at(u, args, w); u += num_pairs) {
+        for (int i = 0; ok && unit_at(i, pair, num_pairs, args, w); ++i) {
             const Problem& p = args.p[w.problem];
             const int row0 = w.mp * kTile + static_cast<int>(rank) * kHalf;
             const int col0 = EPI == kGatedForward ? w.nt * kHalf : w.nt * kTile + static_cast<int>(rank) * kHalf;
@@ -268,7 +287,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
             uint32_t phase = 0;
             uint64_t off = 0;
             bool ok = true;
-            int local = 0;
             // the stages of one unit, operand layouts fixed at compile time so
             // that descriptors, steps and the instruction word stay constants
             // and uniform values
@@ -304,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
                     }
                 }
             };
-            for (int u = pair; ok && unit_at(u, args, w); u += num_pairs, ++local) {
+            for (int local = 0; ok && unit_at(local, pair, num_pairs, args, w); ++local) {
                 const Problem& p = args.p[w.problem];
                 const int buf = local & 1;
                 const uint32_t use = static_cast<uint32_t>(local >> 1);
@@ -330,8 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
         const int quad = warp & 3;          // tensor-memory lane quadrant of this warp
         const int part = (warp - 2) >> 2;   // which share of the columns
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
-        int local = 0;
-        for (int u = pair; unit_at(u, args, w); u += num_pairs, ++local) {
+        for (int local = 0; unit_at(local, pair, num_pairs, args, w); ++local) {
             const Problem& p = args.p[w.problem];
             const int buf = local & 1;
             const uint32_t use = static_cast<uint32_t>(local >> 1);
@@ -409,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
                 }
             } else if (p.split > 1) {
                 // this CTA's half of the fp32 partial: [column / 4][row][4]
-                float* dst = p.part + (static_cast<size_t>(u - p.first_unit) * 2 + rank) * (kHalf * kTile);
+                float* dst = p.part + (static_cast<size_t>(w.index) * 2 + rank) * (kHalf * kTile);
 #pragma unroll 1
                 for (int c = 0; c < kTile; c += 32) {
                     uint32_t r[32];
@@ -498,14 +515,17 @@ int launch_gated(const GatedArgs& args, int num_sms, cudaStream_t stream) {
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-// Column tiles swept together: one while both operands stay in L2, else as
-// many as 48 MiB of B hold (the linear layer's rule, gemm.cu).
-int raster_group(const Problem& p, int64_t k_values) {
-    const double a = static_cast<double>(p.m_pairs) * kTile * k_values * 2.0;
-    const double tile = static_cast<double>(kTile) * k_values * 2.0, b = tile * p.n_tiles;
-    if (a + b <= 192.0 * (1 << 20)) return 1;
-    const int n = static_cast<int>(48.0 * (1 << 20) / tile);
-    return n < 1 ? 1 : (n > p.n_tiles ? p.n_tiles : n);
+// Column tiles swept together (group_n): about sqrt(2 pairs) = 12, so that one
+// wave covers 6 rows x 12 columns of tiles and reads few bytes from HBM for
+// its MMAs, whatever K.  Measured against the linear layer's rule (one column,
+// or as many as 48 MiB of B hold, gemm.cu), TFLOP/s: 32760 x 5120, K = 27648:
+// 1520 against 1380; 8192 x 13824, K = 5120: 1540 against 1510; 13824 x 5120,
+// K = 8192: 1535 against 1292 at one column.
+int raster_group(const Problem& p, int pairs) {
+    int width = 1;
+    while ((width + 1) * (width + 1) <= 2 * pairs) ++width;
+    const int groups = (p.n_tiles + width - 1) / width;
+    return (p.n_tiles + groups - 1) / groups;  // groups of equal width
 }
 
 struct Maps {
@@ -558,10 +578,14 @@ bool ranges_ok(const Range* in, int n_in, const Range* out, int n_out) {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// dX's tiles are few and long (K = 2 D_ff) when there are few tokens: they are
-// cut along K until the launch has a part for every CTA pair, at least eight
-// stages each.
-int dx_split(int64_t M, int64_t D, int64_t F, int pairs) {
+// Stages' worth of time that a unit costs beside its stages (filling the
+// pipeline, its share of the epilogue).
+constexpr int kUnitCost = 8;
+
+// Most parts a dX tile is cut into along K = 2 D_ff: its tiles are few and long
+// when there are few tokens, and then each CTA pair gets at most one part, of at
+// least eight stages.
+int dx_most_parts(int64_t M, int64_t D, int64_t F, int pairs) {
     const int64_t tiles = static_cast<int64_t>(ceil_div(M, kTile)) * ceil_div(D, kTile);
     const int64_t stages = 2 * ceil_div(F, 64);
     int64_t split = pairs / tiles;
@@ -580,7 +604,7 @@ BackwardLayout backward_layout(int64_t M, int64_t D, int64_t F) {
     l.dg = 0;
     l.du = align256(static_cast<size_t>(M) * F * 2);
     l.part = 2 * l.du;
-    const int split = dx_split(M, D, F, kAssumedPairs);
+    const int split = dx_most_parts(M, D, F, kAssumedPairs);
     const size_t units = static_cast<size_t>(ceil_div(M, kTile)) * ceil_div(D, kTile) * split;
     l.total = l.part + (split > 1 ? units * kTile * kTile * sizeof(float) : 0);
     return l;
@@ -621,7 +645,6 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
     GatedArgs args{};
     Maps maps{args};
     args.problems = 1;
-    args.act = act;
     args.err = err;
     Problem& p = args.p[0];
     p.m_pairs = ceil_div(M, kTile);
@@ -632,7 +655,7 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
     p.b0 = p.b1 = maps.add(W_gate, D_ff, D, false);
     maps.add(W_up, D_ff, D, false);
     if (!maps.ok) return RTLYNX_ERR_CUDA;
-    p.group_n = raster_group(p, D);
+    p.group_n = raster_group(p, num_sms / 2);
     p.rows = static_cast<int>(M);
     p.cols = static_cast<int>(D_ff);
     p.out[0] = static_cast<uint16_t*>(H);
@@ -680,7 +703,6 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         GatedArgs args{};
         Maps maps{args};
         args.problems = 1;
-        args.act = act;
         args.err = err;
         Problem& p = args.p[0];
         p.m_pairs = m_pairs;
@@ -691,7 +713,7 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         p.b0 = p.b1 = maps.add(W_down, D, D_ff, true);
         p.b_mn = 1;
         if (!maps.ok) return RTLYNX_ERR_CUDA;
-        p.group_n = raster_group(p, D);
+        p.group_n = raster_group(p, num_sms / 2);
         p.rows = static_cast<int>(M);
         p.cols = static_cast<int>(D_ff);
         p.out[0] = dG;
@@ -706,23 +728,26 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
 
     GatedArgs args{};
     Maps maps{args};
-    args.act = act;
     args.err = err;
-    int dx_index = -1;
-    auto close = [&](Problem& p, int64_t rows, int64_t cols, void* out, int64_t k_values) {
+    const int pairs = num_sms / 2;
+    auto close = [&](Problem& p, int64_t rows, int64_t cols, void* out) {
         p.m_pairs = ceil_div(rows, kTile);
         p.n_tiles = ceil_div(cols, kTile);
         p.rows = static_cast<int>(rows);
         p.cols = static_cast<int>(cols);
         p.out[0] = static_cast<uint16_t*>(out);
-        p.group_n = raster_group(p, k_values);
+        p.group_n = raster_group(p, pairs);
         p.first_unit = args.units;
         args.units += p.m_pairs * p.n_tiles * p.split;
         ++args.problems;
     };
-    if (dX) {
-        Problem& p = args.p[args.problems];
-        dx_index = args.problems;
+    // the weights' gradients: units of token_stages stages each
+    const int64_t w_tiles = static_cast<int64_t>(ceil_div(D_ff, kTile)) * ceil_div(D, kTile);
+    const int64_t shorts = w_tiles * ((dW_gate != nullptr) + (dW_up != nullptr) + (dW_down != nullptr));
+    const int64_t short_cost = token_stages + kUnitCost;
+    const bool has_dx = dX != nullptr;
+    if (has_dx) {
+        Problem& p = args.p[0];
         p.k0 = ceil_div(D_ff, 64);
         p.k = 2 * p.k0;
         p.a0 = maps.add(dG, M, D_ff, false);
@@ -730,9 +755,22 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         p.a1 = maps.add(dU, M, D_ff, false);
         p.b1 = maps.add(W_up, D_ff, D, true);
         p.b_mn = 1;
-        p.split = dx_split(M, D, D_ff, num_sms / 2 < kAssumedPairs ? num_sms / 2 : kAssumedPairs);
+        // cut only while a part is longer than what a CTA pair has to do on average
+        const int64_t tiles = static_cast<int64_t>(m_pairs) * ceil_div(D, kTile);
+        const int64_t average = (tiles * (p.k + kUnitCost) + shorts * short_cost) / pairs + 1;
+        const int64_t wanted = (p.k + kUnitCost + average - 1) / average;
+        const int most = dx_most_parts(M, D, D_ff, pairs < kAssumedPairs ? pairs : kAssumedPairs);
+        p.split = static_cast<int>(wanted < most ? wanted : most);
         p.part = reinterpret_cast<float*>(base + l.part);
-        close(p, M, D, dX, 2 * D_ff);
+        close(p, M, D, dX);
+        args.longs = args.units;
+        // see unit_at: short units that take as long as one dX unit
+        const int rest = args.longs % pairs;
+        if (rest > 0) {
+            int64_t extra = (p.k / p.split + kUnitCost) / short_cost;
+            const int64_t fair = (shorts + pairs - rest - 1) / (pairs - rest);
+            args.extra = static_cast<int>(extra < fair ? extra : fair);
+        }
     }
     auto weight_grad = [&](const void* a, int64_t a_cols, const void* b, int64_t b_cols, void* out) {
         Problem& p = args.p[args.problems];
@@ -741,15 +779,15 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         p.b0 = p.b1 = maps.add(b, M, b_cols, true);
         p.a_mn = p.b_mn = 1;
         p.split = 1;
-        close(p, a_cols, b_cols, out, M);
+        close(p, a_cols, b_cols, out);
     };
     if (dW_gate) weight_grad(dG, D_ff, X, D, dW_gate);
     if (dW_up) weight_grad(dU, D_ff, X, D, dW_up);
     if (dW_down) weight_grad(dY, D, H, D_ff, dW_down);
     if (!maps.ok) return RTLYNX_ERR_CUDA;
     if (launch_gated<kStore, 0>(args, num_sms, stream)) return RTLYNX_ERR_CUDA;
-    if (dx_index >= 0 && args.p[dx_index].split > 1) {
-        const Problem& p = args.p[dx_index];
+    if (has_dx && args.p[0].split > 1) {
+        const Problem& p = args.p[0];
         if (launch_dependent(rtlynx_gated_sum_parts_kernel, dim3(p.m_pairs * p.n_tiles * 2, 16), dim3(256), 0, stream, p))
             return RTLYNX_ERR_CUDA;
     }
