@@ -19,6 +19,7 @@ There is no fallback: if the library is missing every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -369,34 +370,23 @@ def linear(X, W, L_A=None, L_B=None, mode: int = MODE_SPARSE, out=None, stream=N
     return Y
 
 
-class _Launch:
-    """Where a torch-level call runs: the tensors' device, and the stream whose
-    allocator pool its outputs and workspace come from (`stream`, or the
-    device's current one), so that memory is never handed on while in use."""
+_HERE = contextlib.nullcontext()
 
-    def __init__(self, device, stream):
-        import torch
-        self.device, self.ctx = device, None
-        if stream is None:
-            self.handle = int(torch.cuda.current_stream(device).cuda_stream)
-            if torch.cuda.current_device() != device.index:
-                self.ctx = torch.cuda.device(device)
-        else:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            elif stream.device != device:
-                raise ValueError(f"stream of {stream.device}, tensors on {device}")
-            self.handle = int(stream.cuda_stream)
-            self.ctx = torch.cuda.stream(stream)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            return self.ctx.__exit__(*exc)
+def _launch_on(device, stream):
+    """(stream handle, context) of a torch-level call: the tensors' device, and the stream whose allocator pool the
+    call's outputs and workspace come from (`stream`, or the device's current one), so that memory is never handed on
+    while in use."""
+    import torch
+    index = device.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+        return handle, (_HERE if torch.cuda.current_device() == index else torch.cuda.device(device))
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    elif stream.device != device:
+        raise ValueError(f"stream of {stream.device}, tensors on {device}")
+    return int(stream.cuda_stream), torch.cuda.stream(stream)
 
 
 class Rope:
@@ -427,158 +417,167 @@ class Rope:
                            for t in (POS_INT32, POS_INT64, POS_FP32))
 
 
-def _dtype_code(dtype):
+_dtype_codes, _pos_types = {}, {}
+
+
+def _codes(table, names):
+    """Fills a torch dtype -> ABI code table on first use (torch is imported late)."""
     import torch
-    code = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}.get(dtype)
-    if code is None:
-        raise ValueError(f"bf16, fp16 or fp32 tensors, got {dtype}")
-    return code
+    if not table:
+        table.update((getattr(torch, n), i) for i, n in enumerate(names))
+    return table
 
 
-def _heads_view(t, like=None, what="heads"):
-    """HeadsView of t [S, H, D] or [B, S, H, D] (any strides, channels contiguous)."""
-    if not t.is_cuda or t.dim() not in (3, 4) or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{what}: CUDA tensor [S, H, D] or [B, S, H, D] with contiguous channels")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{what}: {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
-    st = t.stride()
-    return HeadsView(t.data_ptr(), t.shape[-2], st[0] if t.dim() == 4 else 0, st[-3], st[-2])
+def _heads_view(t, shape, dtype, device, what):
+    """HeadsView of t [S, H, D] or [B, S, H, D] (any strides, channels contiguous), checked against the first tensor's
+    dtype, device and shape (the heads aside, where shape has None)."""
+    st, sh = t.stride(), t.shape
+    n = len(sh)
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what}: {t.dtype} on {t.device}, expected {dtype} on {device}")
+    if n != len(shape) or sh[-1] != shape[-1] or sh[0] != shape[0] or sh[-3] != shape[-3] or \
+            (shape[-2] is not None and sh[-2] != shape[-2]):
+        raise ValueError(f"{what}: shape {tuple(sh)}, expected {tuple(shape)}")
+    if st[-1] != 1 and sh[-1] > 1:
+        raise ValueError(f"{what}: the channels of a head are contiguous, got strides {st}")
+    return HeadsView(t.data_ptr(), sh[-2], st[0] if n == 4 else 0, st[-3], st[-2])
 
 
-def _heads_out(out, like, what):
-    import torch
-    if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    if out.shape != like.shape:
-        raise ValueError(f"{what}: shape {tuple(out.shape)}, expected {tuple(like.shape)}")
-    return out
+class _HeadsCall:
+    """The checked arguments that every query/key call shares."""
+
+    __slots__ = ("shape", "kshape", "dtype", "device", "B", "S", "D", "code", "spec", "strides", "handle", "ctx")
+
+    def __init__(self, q, k, positions, rope, stream):
+        shape = q.shape
+        n = len(shape)
+        if n not in (3, 4) or not q.is_cuda:
+            raise ValueError(f"CUDA tensors [S, H, D] or [B, S, H, D], got {tuple(shape)} on {q.device}")
+        self.shape, self.dtype, self.device = shape, q.dtype, q.device
+        self.kshape = None if k is None else (*shape[:-2], None, shape[-1])
+        self.B, S, self.D = (shape[0] if n == 4 else 1), shape[-3], shape[-1]
+        self.S = S
+        self.code = (_dtype_codes or _codes(_dtype_codes, ("bfloat16", "float16", "float32"))).get(self.dtype)
+        if self.code is None:
+            raise ValueError(f"bf16, fp16 or fp32 tensors, got {self.dtype}")
+        # positions [S, axes], shared by the sequences, or [B, S, axes]
+        kind = (_pos_types or _codes(_pos_types, ("int32", "int64", "float32"))).get(positions.dtype)
+        if kind is None or positions.device != self.device:
+            raise ValueError(f"positions: int32, int64 or float32 on {self.device}, got {positions.dtype} on "
+                             f"{positions.device}")
+        at, axes = positions.shape, len(rope.axes)
+        if at == (S, axes):
+            self.strides = (0, *positions.stride())
+        elif at == (self.B, S, axes):
+            self.strides = positions.stride()
+        else:
+            raise ValueError(f"positions {tuple(at)}, expected {(S, axes)} or {(self.B, S, axes)}")
+        self.spec = rope.specs[kind]
+        self.handle, self.ctx = _launch_on(self.device, stream)
+
+    def view(self, t, what, keys=False):
+        if t is None:
+            return None
+        return _heads_view(t, self.kshape if keys else self.shape, self.dtype, self.device, what)
+
+    def weight(self, w, what):
+        if w is None:
+            return None
+        if w.shape != (self.D,) or w.dtype != self.dtype or w.device != self.device or not w.is_contiguous():
+            raise ValueError(f"{what}: contiguous [{self.D}] {self.dtype} on {self.device}")
+        return w.data_ptr()
+
+    def outputs(self, out, q, k):
+        import torch
+        if out is None:
+            plain = torch.contiguous_format
+            out = torch.empty_like(q, memory_format=plain), \
+                None if k is None else torch.empty_like(k, memory_format=plain)
+        return out[0], None if k is None else out[1]
 
 
-def _heads_sizes(q, k):
-    B = q.shape[0] if q.dim() == 4 else 1
-    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]):
-        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} differ in more than their heads")
-    return B, q.shape[-3], q.shape[-1]
-
-
-def _rope_positions(positions, rope, q, B, S):
-    """(spec, positions, strides) for positions [S, axes] or [B, S, axes]."""
-    import torch
-    kind = {torch.int32: POS_INT32, torch.int64: POS_INT64, torch.float32: POS_FP32}.get(positions.dtype)
-    if kind is None or positions.device != q.device:
-        raise ValueError(f"positions: int32, int64 or float32 on {q.device}, got {positions.dtype} on "
-                         f"{positions.device}")
-    shape, st = tuple(positions.shape), positions.stride()
-    if shape == (S, len(rope.axes)):
-        strides = (0, st[0], st[1])
-    elif shape == (B, S, len(rope.axes)):
-        strides = st
-    else:
-        raise ValueError(f"positions {shape}, expected {(S, len(rope.axes))} or {(B, S, len(rope.axes))}")
-    return rope.specs[kind], strides
-
-
-def _norm_weight(w, q, what):
-    if w is not None and (tuple(w.shape) != (q.shape[-1],) or w.dtype != q.dtype or w.device != q.device or
-                          not w.is_contiguous()):
-        raise ValueError(f"{what}: contiguous [{q.shape[-1]}] {q.dtype} on {q.device}")
-    return w
-
-
-def _run_rope(q, k, positions, rope, out, stream, backward):
-    qv = _heads_view(q, what="q")
-    kv = None if k is None else _heads_view(k, q, "k")
-    code = _dtype_code(q.dtype)
-    B, S, D = _heads_sizes(q, k)
-    spec, strides = _rope_positions(positions, rope, q, B, S)
-    with _Launch(q.device, stream) as handle:
-        q_out = _heads_out(out[0] if out else None, q, "q_out")
-        k_out = None if k is None else _heads_out(out[1] if out else None, k, "k_out")
-        call = rtlynx_rope_backward if backward else rtlynx_rope
-        call(qv, kv, _heads_view(q_out, q, "q_out"), None if k is None else _heads_view(k_out, q, "k_out"), B, S, D,
-             code, spec, positions, strides, handle)
-    return q_out, k_out
+def _run_rope(name, q, k, positions, rope, out, stream):
+    c = _HeadsCall(q, k, positions, rope, stream)
+    with c.ctx:
+        qo, ko = c.outputs(out, q, k)
+        status = getattr(lib(), name)(
+            c.view(q, "q"), c.view(k, "k", True), c.view(qo, "q_out"), None if ko is None else
+            _heads_view(ko, k.shape, c.dtype, c.device, "k_out"), c.B, c.S, c.D, c.code, c.spec, positions.data_ptr(),
+            *c.strides, c.handle)
+    _check(status, name)
+    return qo, ko
 
 
 def rope(q, k, positions, rope, out=None, stream=None):
     """(R q, R k) for q [B, S, Hq, D] and k [B, S, Hk, D] (or [S, H, D], or k None), any strides.
 
     positions [S, axes] or [B, S, axes] (int32, int64, float32), rope a Rope; out=(q, k) works in place."""
-    return _run_rope(q, k, positions, rope, out, stream, False)
+    return _run_rope("rtlynx_rope", q, k, positions, rope, out, stream)
 
 
 def rope_backward(dq_out, dk_out, positions, rope, out=None, stream=None):
     """Gradients of rope()'s inputs from those of its outputs; out=(dq_out, dk_out) works in place."""
-    return _run_rope(dq_out, dk_out, positions, rope, out, stream, True)
+    return _run_rope("rtlynx_rope_backward", dq_out, dk_out, positions, rope, out, stream)
 
 
 def qk_norm_rope(q, k, w_q, w_k, positions, rope, eps=1e-6, out=None, stream=None):
     """rope() of the heads' RMS norms: (R (w_q q / rms q), R (w_k k / rms k)); w_q, w_k [D] in q's type, or None."""
-    qv = _heads_view(q, what="q")
-    kv = None if k is None else _heads_view(k, q, "k")
-    code = _dtype_code(q.dtype)
-    B, S, D = _heads_sizes(q, k)
-    spec, strides = _rope_positions(positions, rope, q, B, S)
-    _norm_weight(w_q, q, "w_q")
-    _norm_weight(w_k, q, "w_k")
-    with _Launch(q.device, stream) as handle:
-        q_out = _heads_out(out[0] if out else None, q, "q_out")
-        k_out = None if k is None else _heads_out(out[1] if out else None, k, "k_out")
-        rtlynx_qk_norm_rope(qv, kv, w_q, w_k, _heads_view(q_out, q, "q_out"),
-                            None if k is None else _heads_view(k_out, q, "k_out"), B, S, D, code, eps, spec,
-                            positions, strides, handle)
-    return q_out, k_out
+    c = _HeadsCall(q, k, positions, rope, stream)
+    with c.ctx:
+        qo, ko = c.outputs(out, q, k)
+        status = lib().rtlynx_qk_norm_rope(
+            c.view(q, "q"), c.view(k, "k", True), c.weight(w_q, "w_q"), c.weight(w_k, "w_k"), c.view(qo, "q_out"),
+            None if ko is None else _heads_view(ko, k.shape, c.dtype, c.device, "k_out"), c.B, c.S, c.D, c.code, eps,
+            c.spec, positions.data_ptr(), *c.strides, c.handle)
+    _check(status, "rtlynx_qk_norm_rope")
+    return qo, ko
 
 
 def qk_norm_rope_backward(dq_out, dk_out, q, k, w_q, w_k, positions, rope, eps=1e-6, out=None, weight_grads=True,
                           stream=None):
-    """(dq, dk, dw_q, dw_k) of qk_norm_rope(); dw_q, dw_k are float32 [D], None without weight_grads or a weight."""
+    """(dq, dk, dw_q, dw_k) of qk_norm_rope(); dw_q, dw_k are float32 [D], None without weight_grads or a weight.
+
+    out=(dq_out, dk_out) or out=(q, k) works in place."""
     import torch
-    qv, gqv = _heads_view(q, what="q"), _heads_view(dq_out, q, "dq_out")
-    kv = None if k is None else _heads_view(k, q, "k")
-    if (dk_out is None) != (k is None) or dq_out.shape != q.shape or (k is not None and dk_out.shape != k.shape):
-        raise ValueError("dq_out and dk_out have the shapes of q and k")
-    gkv = None if k is None else _heads_view(dk_out, q, "dk_out")
-    code = _dtype_code(q.dtype)
-    B, S, D = _heads_sizes(q, k)
-    spec, strides = _rope_positions(positions, rope, q, B, S)
-    _norm_weight(w_q, q, "w_q")
-    _norm_weight(w_k, q, "w_k")
-    with _Launch(q.device, stream) as handle:
-        dq = _heads_out(out[0] if out else None, q, "dq")
-        dk = None if k is None else _heads_out(out[1] if out else None, k, "dk")
-        dw_q = dw_k = ws = None
-        if weight_grads and w_q is not None:
-            dw_q = torch.empty(D, dtype=torch.float32, device=q.device)
-        if weight_grads and w_k is not None and k is not None:
-            dw_k = torch.empty(D, dtype=torch.float32, device=q.device)
-        ws_bytes = 0
+    if (dk_out is None) != (k is None):
+        raise ValueError("dk_out goes with k")
+    c = _HeadsCall(q, k, positions, rope, stream)
+    with c.ctx:
+        dq, dk = c.outputs(out, q, k)
+        dw_q = torch.empty(c.D, dtype=torch.float32, device=c.device) if weight_grads and w_q is not None else None
+        dw_k = torch.empty(c.D, dtype=torch.float32, device=c.device) \
+            if weight_grads and w_k is not None and k is not None else None
+        ws, ws_bytes = None, 0
         if dw_q is not None or dw_k is not None:
-            ws_bytes = rtlynx_qk_norm_rope_workspace_size(D)
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        rtlynx_qk_norm_rope_backward(gqv, gkv, qv, kv, w_q, w_k, _heads_view(dq, q, "dq"),
-                                     None if k is None else _heads_view(dk, q, "dk"), dw_q, dw_k, B, S, D, code, eps,
-                                     spec, positions, strides, ws, ws_bytes, handle)
+            ws_bytes = rtlynx_qk_norm_rope_workspace_size(c.D)
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=c.device)
+
+        def like_k(t, what):
+            return None if k is None else _heads_view(t, k.shape, c.dtype, c.device, what)
+
+        status = lib().rtlynx_qk_norm_rope_backward(
+            c.view(dq_out, "dq_out"), like_k(dk_out, "dk_out"), c.view(q, "q"), c.view(k, "k", True),
+            c.weight(w_q, "w_q"), c.weight(w_k, "w_k"), c.view(dq, "dq"), like_k(dk, "dk"), _ptr(dw_q), _ptr(dw_k),
+            c.B, c.S, c.D, c.code, eps, c.spec, positions.data_ptr(), *c.strides, _ptr(ws), ws_bytes, c.handle)
+    _check(status, "rtlynx_qk_norm_rope_backward")
     return dq, dk, dw_q, dw_k
 
 
-def _matrix(t, shape, device, what):
-    """t, checked: a contiguous bf16 CUDA matrix of this shape on this device."""
+def _matrix(t, rows, cols, device, what):
+    """The address of t, checked: a contiguous bf16 CUDA matrix of this shape on this device."""
     import torch
-    if t.dtype != torch.bfloat16 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: contiguous bf16 {shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t
+    if t.dtype != torch.bfloat16 or t.device != device or t.shape != (rows, cols) or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous bf16 {(rows, cols)} on {device}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+    return t.data_ptr()
 
 
-def _gated_sizes(X, W_gate, W_up, W_down):
+def _gated_inputs(X, W_gate, W_up, W_down):
     if not X.is_cuda or X.dim() != 2 or W_gate.dim() != 2:
         raise ValueError("X [M, D] and W_gate [D_ff, D] are CUDA matrices")
-    (M, D), D_ff = X.shape, W_gate.shape[0]
-    _matrix(X, (M, D), X.device, "X")
-    _matrix(W_gate, (D_ff, D), X.device, "W_gate")
-    _matrix(W_up, (D_ff, D), X.device, "W_up")
-    _matrix(W_down, (D, D_ff), X.device, "W_down")
-    return M, D, D_ff
+    (M, D), F, device = X.shape, W_gate.shape[0], X.device
+    return (M, D, F), (_matrix(X, M, D, device, "X"), _matrix(W_gate, F, D, device, "W_gate"),
+                       _matrix(W_up, F, D, device, "W_up"), _matrix(W_down, D, F, device, "W_down"))
 
 
 def gated_mlp(X, W_gate, W_up, W_down, act=ACT_SILU, L_A=None, L_B=None, mode_down=MODE_DENSE_SKIP, save=False,
@@ -589,17 +588,23 @@ def gated_mlp(X, W_gate, W_up, W_down, act=ACT_SILU, L_A=None, L_B=None, mode_do
     With mode_down=MODE_SPARSE the down-projection is the activation-sparse layer with the LoRA pair L_A [D, R],
     L_B [R, D_ff].  With save=True the result is (Y, saved), saved = (G, U, H) for gated_mlp_backward."""
     import torch
-    M, D, D_ff = _gated_sizes(X, W_gate, W_up, W_down)
+    (M, D, F), at = _gated_inputs(X, W_gate, W_up, W_down)
+    device = X.device
     R = 0 if (L_A is None or L_B is None or mode_down == MODE_DENSE_SKIP) else L_B.shape[0]
-    if R:
-        _matrix(L_A, (D, R), X.device, "L_A")
-        _matrix(L_B, (R, D_ff), X.device, "L_B")
-    with _Launch(X.device, stream) as handle:
-        Y = torch.empty((M, D), dtype=X.dtype, device=X.device) if out is None else _matrix(out, (M, D), X.device, "out")
-        H = torch.empty((M, D_ff), dtype=X.dtype, device=X.device)
+    la = _matrix(L_A, D, R, device, "L_A") if R else None
+    lb = _matrix(L_B, R, F, device, "L_B") if R else None
+    handle, ctx = _launch_on(device, stream)
+    with ctx:
+        if out is None:
+            Y = torch.empty_like(X)
+            y = Y.data_ptr()
+        else:
+            Y, y = out, _matrix(out, M, D, device, "out")
+        H = torch.empty((M, F), dtype=X.dtype, device=device)
         G, U = (torch.empty_like(H), torch.empty_like(H)) if save else (None, None)
-        rtlynx_gated_mlp_block(X, W_gate, W_up, W_down, L_A if R else None, L_B if R else None, G, U, H, Y, M, D, D_ff,
-                               R, act, mode_down, handle)
+        status = lib().rtlynx_gated_mlp_block(*at, la, lb, _ptr(G), _ptr(U), H.data_ptr(), y, M, D, F, R, act,
+                                              mode_down, handle)
+    _check(status, "rtlynx_gated_mlp_block")
     return (Y, (G, U, H)) if save else Y
 
 
@@ -608,13 +613,16 @@ def gated_mlp_backward(dY, X, W_gate, W_up, W_down, saved, act=ACT_SILU, needs=(
 
     needs: which of the four to compute; the others are None."""
     import torch
-    M, D, D_ff = _gated_sizes(X, W_gate, W_up, W_down)
-    _matrix(dY, (M, D), X.device, "dY")
-    for t, name in zip(saved, "GUH"):
-        _matrix(t, (M, D_ff), X.device, name)
-    with _Launch(X.device, stream) as handle:
+    (M, D, F), at = _gated_inputs(X, W_gate, W_up, W_down)
+    device = X.device
+    dy = _matrix(dY, M, D, device, "dY")
+    kept = [_matrix(t, M, F, device, name) for t, name in zip(saved, "GUH")]
+    handle, ctx = _launch_on(device, stream)
+    with ctx:
         grads = tuple(torch.empty_like(t) if need else None for t, need in zip((X, W_gate, W_up, W_down), needs))
-        ws_bytes = rtlynx_gated_mlp_backward_workspace_size(M, D, D_ff)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=X.device)
-        rtlynx_gated_mlp_backward(dY, X, W_gate, W_up, W_down, *saved, *grads, M, D, D_ff, act, ws, ws_bytes, handle)
+        ws_bytes = rtlynx_gated_mlp_backward_workspace_size(M, D, F)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+        status = lib().rtlynx_gated_mlp_backward(dy, *at, *kept, *(_ptr(g) for g in grads), M, D, F, act,
+                                                 ws.data_ptr(), ws_bytes, handle)
+    _check(status, "rtlynx_gated_mlp_backward")
     return grads
