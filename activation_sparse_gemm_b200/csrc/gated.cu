@@ -641,6 +641,16 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
     rc = device_info(&num_sms, &err);
     if (rc) return rc;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    if (M <= kFewTokens) {
+        if (launch_gated_few(X, W_gate, W_up, H, G, U, static_cast<int>(M), static_cast<int>(D),
+                             static_cast<int>(D_ff), act, stream))
+            return RTLYNX_ERR_CUDA;
+        if (mode_down == RTLYNX_MODE_SPARSE)
+            return rtlynx_linear(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down, stream_);
+        return launch_down_few(H, W_down, Y, static_cast<int>(M), static_cast<int>(D_ff), static_cast<int>(D), stream)
+                   ? RTLYNX_ERR_CUDA
+                   : RTLYNX_OK;
+    }
 
     GatedArgs args{};
     Maps maps{args};
