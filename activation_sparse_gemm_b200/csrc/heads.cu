@@ -16,7 +16,13 @@
 // computed or loaded once a token and stay in registers, and no table of
 // angles is read.  Eight channels are 16 bytes of a 16-bit type; a head of d
 // channels takes d / 8 lanes, and several heads share a pass of the warp when
-// d <= 128.  kUnroll passes are loaded before the first is used.
+// d <= 128.  Pairs are computed two at a time (f32x2): the norm's gradient
+// took 195 us without.
+//
+// Measured (32760 tokens, 40 + 40 heads of 128, bf16, 1.34 GB): rotation 207 us
+// (6.5 TB/s, the measured copy rate), with the norm 229 us (5.9 TB/s); gradient
+// of both on 16384 tokens (1.01 GB) 179 us (5.6 TB/s).  One warp for a token's
+// queries and keys, with the angles computed once for both, changed nothing.
 //
 // Angles: position x frequency / 2 pi in 64 bits, reduced to an eighth of a
 // turn there, so a position of 2^24 loses nothing; sine and cosine of the
@@ -74,10 +80,45 @@ struct Raw {
     uint32_t r[2 * sizeof(T)];
 };
 
-__device__ __forceinline__ float2 widen(uint32_t u, __nv_bfloat16) {
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+// Two floats in one 64-bit register: sm_100 multiplies and adds both at once.
+using F2 = unsigned long long;
+
+__device__ __forceinline__ F2 make_f2(float lo, float hi) {
+    F2 v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
 }
-__device__ __forceinline__ float2 widen(uint32_t u, __half) { return __half22float2(*reinterpret_cast<__half2*>(&u)); }
+__device__ __forceinline__ float lo(F2 v) {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return a;
+}
+__device__ __forceinline__ float hi(F2 v) {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return b;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+    F2 v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+    F2 v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ F2 negate(F2 v) { return v ^ 0x8000000080000000ull; }
+
+__device__ __forceinline__ float widen_lo(uint32_t u, __nv_bfloat16) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float widen_hi(uint32_t u, __nv_bfloat16) { return __uint_as_float(u & 0xFFFF0000u); }
+__device__ __forceinline__ float widen_lo(uint32_t u, __half) { return __low2float(*reinterpret_cast<__half2*>(&u)); }
+__device__ __forceinline__ float widen_hi(uint32_t u, __half) { return __high2float(*reinterpret_cast<__half2*>(&u)); }
 
 __device__ __forceinline__ uint32_t narrow(float a, float b, __nv_bfloat16) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -88,30 +129,53 @@ __device__ __forceinline__ uint32_t narrow(float a, float b, __half) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-template <typename T>
-__device__ __forceinline__ void unpack(const Raw<T>& raw, float (&v)[8]) {
-    if constexpr (sizeof(T) == 4) {
+// A lane's four pairs: x[i] holds the first channels of pairs 2 i and 2 i + 1,
+// y[i] the second ones.
+struct Pairs {
+    F2 x[2], y[2];
+};
+
+template <typename T, bool HALF>
+__device__ __forceinline__ Pairs unpack(const Raw<T>& raw) {
+    Pairs p;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(raw.r[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = widen(raw.r[j], T());
-            v[2 * j] = f.x;
-            v[2 * j + 1] = f.y;
+    for (int i = 0; i < 2; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            const uint32_t* r = raw.r;
+            const int x0 = HALF ? 2 * i : 4 * i, x1 = HALF ? 2 * i + 1 : 4 * i + 2, y = HALF ? 4 : 1;
+            p.x[i] = make_f2(__uint_as_float(r[x0]), __uint_as_float(r[x1]));
+            p.y[i] = make_f2(__uint_as_float(r[x0 + y]), __uint_as_float(r[x1 + y]));
+        } else if constexpr (HALF) {
+            p.x[i] = make_f2(widen_lo(raw.r[i], T()), widen_hi(raw.r[i], T()));
+            p.y[i] = make_f2(widen_lo(raw.r[2 + i], T()), widen_hi(raw.r[2 + i], T()));
+        } else {
+            p.x[i] = make_f2(widen_lo(raw.r[2 * i], T()), widen_lo(raw.r[2 * i + 1], T()));
+            p.y[i] = make_f2(widen_hi(raw.r[2 * i], T()), widen_hi(raw.r[2 * i + 1], T()));
         }
     }
+    return p;
 }
 
-template <typename T>
-__device__ __forceinline__ void pack(const float (&v)[8], Raw<T>& raw) {
-    if constexpr (sizeof(T) == 4) {
+template <typename T, bool HALF>
+__device__ __forceinline__ Raw<T> pack(const Pairs& p) {
+    Raw<T> raw;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) raw.r[j] = __float_as_uint(v[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) raw.r[j] = narrow(v[2 * j], v[2 * j + 1], T());
+    for (int i = 0; i < 2; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            const int x0 = HALF ? 2 * i : 4 * i, x1 = HALF ? 2 * i + 1 : 4 * i + 2, y = HALF ? 4 : 1;
+            raw.r[x0] = __float_as_uint(lo(p.x[i]));
+            raw.r[x1] = __float_as_uint(hi(p.x[i]));
+            raw.r[x0 + y] = __float_as_uint(lo(p.y[i]));
+            raw.r[x1 + y] = __float_as_uint(hi(p.y[i]));
+        } else if constexpr (HALF) {
+            raw.r[i] = narrow(lo(p.x[i]), hi(p.x[i]), T());
+            raw.r[2 + i] = narrow(lo(p.y[i]), hi(p.y[i]), T());
+        } else {
+            raw.r[2 * i] = narrow(lo(p.x[i]), lo(p.y[i]), T());
+            raw.r[2 * i + 1] = narrow(hi(p.x[i]), hi(p.y[i]), T());
+        }
     }
+    return raw;
 }
 
 // A lane's eight channels are two runs of four, at offsets a and b.  They
@@ -146,18 +210,22 @@ __device__ __forceinline__ void store8(T* p, int a, int b, const Raw<T>& raw) {
     }
 }
 
-// Turns the lane's four pairs; pairs that are not rotated keep their bits
-// (multiplying by a sine of zero would make NaN of an infinity).
-template <bool HALF>
-__device__ __forceinline__ void rotate(float (&v)[8], const float (&c)[4], const float (&s)[4], uint32_t turned) {
+// Turns the lane's four pairs: (x, y) -> (x a - y b, x c + y d).  Where not the
+// whole head is turned, the other pairs are (x a, y d): their b and c are zero,
+// but zero times an infinity in the other channel would be NaN.
+__device__ __forceinline__ void turn(Pairs& p, const F2 (&a)[2], const F2 (&nb)[2], const F2 (&c)[2], const F2 (&d)[2],
+                                     bool whole, uint32_t turned) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int a = HALF ? j : 2 * j, b = HALF ? j + 4 : 2 * j + 1;
-        const float x = v[a], y = v[b];
-        if (turned >> j & 1u) {
-            v[a] = fmaf(x, c[j], -y * s[j]);
-            v[b] = fmaf(x, s[j], y * c[j]);
+    for (int i = 0; i < 2; ++i) {
+        const F2 x = mul(p.x[i], a[i]), y = mul(p.y[i], d[i]);
+        F2 tx = fma2(p.y[i], nb[i], x), ty = fma2(p.x[i], c[i], y);
+        if (!whole) {
+            const bool t0 = turned >> (2 * i) & 1u, t1 = turned >> (2 * i + 1) & 1u;
+            tx = make_f2(t0 ? lo(tx) : lo(x), t1 ? hi(tx) : hi(x));
+            ty = make_f2(t0 ? lo(ty) : lo(y), t1 ? hi(ty) : hi(y));
         }
+        p.x[i] = tx;
+        p.y[i] = ty;
     }
 }
 
@@ -169,9 +237,17 @@ __device__ __forceinline__ float head_sum(float v) {
 }
 
 template <typename T, int LANES, bool HALF, int KIND>
-__global__ void __launch_bounds__(kHeadThreads) rtlynx_heads_kernel(const __grid_constant__ HeadArgs args) {
+__global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) rtlynx_heads_kernel(const __grid_constant__ HeadArgs args) {
     constexpr int kHeadsPerPass = 32 / LANES;
-    constexpr int kUnroll = sizeof(T) == 4 ? 2 : (KIND == kNormBackward ? 2 : 4);
+    // Passes loaded before the first is used, and whether the next ones are
+    // loaded before these are computed.  Registers decide: forward, 64 of them
+    // leave 32 warps an SM, which hide the latency without looking ahead
+    // (video workload's norm: 229 us; two passes and looking ahead 235, 80
+    // registers 249); backward, with two tensors read and the weights' sums
+    // kept, 128 and 16 warps, looking ahead (179 us; without 205, two passes 190).
+    constexpr int kUnroll = 4 / (sizeof(T) == 4 ? 2 : 1);
+    constexpr int kGrads = KIND == kNormBackward ? kUnroll : 1;
+    constexpr bool kPipe = KIND == kNormBackward;
     __shared__ double turns[kMaxPairs];
     __shared__ uint8_t axis[kMaxPairs];
     __shared__ float sums[KIND == kNormBackward ? kHeadWarps * 32 * 8 : 1];
@@ -191,6 +267,7 @@ __global__ void __launch_bounds__(kHeadThreads) rtlynx_heads_kernel(const __grid
     const int chunk = lane % LANES, sub = lane / LANES;
     const bool active = chunk * 8 < args.dim;
     const int rotated = 2 * args.pairs;
+    const bool whole = rotated == args.dim;
     // channel offsets of the lane's two runs of four
     int a = 8 * chunk, b = 8 * chunk + 4;
     if (HALF && 8 * chunk < rotated) {
@@ -198,19 +275,17 @@ __global__ void __launch_bounds__(kHeadThreads) rtlynx_heads_kernel(const __grid
         b = args.pairs + 4 * chunk;
     }
 
-    float w[8];
-    if constexpr (KIND != kRope) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+    const F2 one = make_f2(1.0f, 1.0f), zero = make_f2(0.0f, 0.0f);
+    Pairs w{{one, one}, {one, one}};
+    auto load_weights = [&]() {
         if (active && t.w) {
             Raw<T> raw;
             load8<T, HALF>(static_cast<const T*>(t.w), a, b, raw);
-            unpack<T>(raw, w);
+            w = unpack<T, HALF>(raw);
         }
-    }
-    float dw[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[j] = 0.0f;
+    };
+    if constexpr (KIND == kNormBackward) load_weights();
+    Pairs dw{{zero, zero}, {zero, zero}};
     const float inv_dim = 1.0f / static_cast<float>(args.dim);
 
     for (uint32_t item = block * kHeadWarps + warp; item < t.items; item += t.blocks * kHeadWarps) {
@@ -245,77 +320,119 @@ __global__ void __launch_bounds__(kHeadThreads) rtlynx_heads_kernel(const __grid
                 turned |= 1u << j;
             }
         }
+        // the turn's coefficients; the norm's weights are part of them going
+        // forward (and not kept beside them)
+        if constexpr (KIND == kNorm) load_weights();
+        F2 ca[2], nb[2], cc[2], cd[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const F2 c2 = make_f2(c[2 * i], c[2 * i + 1]), s2 = make_f2(s[2 * i], s[2 * i + 1]);
+            ca[i] = cd[i] = c2;
+            cc[i] = s2;
+            nb[i] = negate(s2);
+            if constexpr (KIND == kNorm) {
+                ca[i] = mul(ca[i], w.x[i]);
+                cc[i] = mul(cc[i], w.x[i]);
+                nb[i] = mul(nb[i], w.y[i]);
+                cd[i] = mul(cd[i], w.y[i]);
+            }
+        }
 
         const T* x = static_cast<const T*>(t.x) + bi * t.xb + si * t.xs;
         const T* dy = KIND == kNormBackward ? static_cast<const T*>(t.dy) + bi * t.gb + si * t.gs : nullptr;
         T* y = static_cast<T*>(t.y) + bi * t.yb + si * t.ys;
         const uint32_t first = group * t.passes * kHeadsPerPass;
         const uint32_t last = min(first + t.passes * kHeadsPerPass, t.heads);
-        for (uint32_t h0 = first; h0 < last; h0 += kHeadsPerPass * kUnroll) {
-            Raw<T> rx[kUnroll], rg[KIND == kNormBackward ? kUnroll : 1];
+        auto fetch = [&](uint32_t h0, Raw<T>(&rx)[kUnroll], Raw<T>(&rg)[kGrads]) {
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const uint32_t h = h0 + u * kHeadsPerPass + sub;
 #pragma unroll
                 for (int j = 0; j < static_cast<int>(2 * sizeof(T)); ++j) {
                     rx[u].r[j] = 0u;
-                    if (KIND == kNormBackward) rg[u].r[j] = 0u;
+                    if (KIND == kNormBackward) rg[u % kGrads].r[j] = 0u;
                 }
                 if (active && h < last) {
                     load8<T, HALF>(x + h * t.xh, a, b, rx[u]);
                     if constexpr (KIND == kNormBackward) load8<T, HALF>(dy + h * t.gh, a, b, rg[u]);
                 }
             }
+        };
+        Raw<T> rx[kUnroll], rg[kGrads];
+        if (kPipe) fetch(first, rx, rg);
+        for (uint32_t h0 = first; h0 < last; h0 += kHeadsPerPass * kUnroll) {
+            Raw<T> nx[kUnroll], ng[kGrads];
+            if (kPipe)
+                fetch(h0 + kHeadsPerPass * kUnroll, nx, ng);
+            else
+                fetch(h0, rx, rg);
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
+            for (int u = 0; u < kUnroll; ++u) {  // heads past the last are zeros, and not stored
                 const uint32_t h = h0 + u * kHeadsPerPass + sub;
-                if (h0 + u * kHeadsPerPass >= last) break;  // the same in the whole warp
-                float v[8];
-                unpack<T>(rx[u], v);
+                Pairs v = unpack<T, HALF>(rx[u]);
                 if constexpr (KIND == kRope) {
-                    rotate<HALF>(v, c, s, turned);
+                    turn(v, ca, nb, cc, cd, whole, turned);
                 } else {
-                    float squares = 0.0f;
+                    const F2 squares = fma2(v.y[1], v.y[1], fma2(v.x[1], v.x[1], fma2(v.y[0], v.y[0], mul(v.x[0], v.x[0]))));
+                    const float r = rsqrtf(fmaf(head_sum<LANES>(lo(squares) + hi(squares)), inv_dim, args.eps));
+                    const F2 r2 = make_f2(r, r);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) squares = fmaf(v[j], v[j], squares);
-                    const float r = rsqrtf(fmaf(head_sum<LANES>(squares), inv_dim, args.eps));
+                    for (int i = 0; i < 2; ++i) {  // n
+                        v.x[i] = mul(v.x[i], r2);
+                        v.y[i] = mul(v.y[i], r2);
+                    }
                     if constexpr (KIND == kNorm) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] *= r * w[j];
-                        rotate<HALF>(v, c, s, turned);
+                        turn(v, ca, nb, cc, cd, whole, turned);
                     } else {
-                        float g[8];
-                        unpack<T>(rg[u], g);
-                        rotate<HALF>(g, c, s, turned);
-                        float dot = 0.0f;
+                        Pairs g = unpack<T, HALF>(rg[u]);
+                        turn(g, ca, nb, cc, cd, whole, turned);
+                        F2 dot = zero;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            v[j] *= r;  // n
-                            dw[j] = fmaf(g[j], v[j], dw[j]);
-                            g[j] *= w[j];
-                            dot = fmaf(g[j], v[j], dot);
+                        for (int i = 0; i < 2; ++i) {
+                            dw.x[i] = fma2(g.x[i], v.x[i], dw.x[i]);
+                            dw.y[i] = fma2(g.y[i], v.y[i], dw.y[i]);
+                            g.x[i] = mul(g.x[i], w.x[i]);
+                            g.y[i] = mul(g.y[i], w.y[i]);
+                            dot = fma2(g.x[i], v.x[i], dot);
+                            dot = fma2(g.y[i], v.y[i], dot);
                         }
-                        const float mean = head_sum<LANES>(dot) * inv_dim;
+                        const float mean = -head_sum<LANES>(lo(dot) + hi(dot)) * inv_dim;
+                        const F2 mean2 = make_f2(mean, mean);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] = r * fmaf(-v[j], mean, g[j]);
+                        for (int i = 0; i < 2; ++i) {
+                            v.x[i] = mul(r2, fma2(v.x[i], mean2, g.x[i]));
+                            v.y[i] = mul(r2, fma2(v.y[i], mean2, g.y[i]));
+                        }
                     }
                 }
-                if (active && h < last) {
-                    Raw<T> out;
-                    pack<T>(v, out);
-                    store8<T, HALF>(y + h * t.yh, a, b, out);
-                }
+                if (active && h < last) store8<T, HALF>(y + h * t.yh, a, b, pack<T, HALF>(v));
+            }
+            if (kPipe) {
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) rx[u] = nx[u];
+#pragma unroll
+                for (int u = 0; u < kGrads; ++u) rg[u] = ng[u];
             }
         }
     }
 
     if constexpr (KIND == kNormBackward) {
-        // heads that shared a pass hold the same channels in different lanes
+        // Heads that shared a pass hold the same channels in different lanes.
+        // In channel order: the lane's runs of four at a and at b.
+        float sum[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int x0 = HALF ? 2 * i : 4 * i, x1 = HALF ? 2 * i + 1 : 4 * i + 2, to_y = HALF ? 4 : 1;
+            sum[x0] = lo(dw.x[i]);
+            sum[x1] = hi(dw.x[i]);
+            sum[x0 + to_y] = lo(dw.y[i]);
+            sum[x1 + to_y] = hi(dw.y[i]);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
 #pragma unroll
-            for (int m = LANES; m < 32; m <<= 1) dw[j] += __shfl_xor_sync(0xFFFFFFFFu, dw[j], m);
-            if (sub == 0) sums[(warp * 32 + chunk) * 8 + j] = dw[j];
+            for (int m = LANES; m < 32; m <<= 1) sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], m);
+            if (sub == 0) sums[(warp * 32 + chunk) * 8 + j] = sum[j];
         }
         __syncthreads();
         if (t.part && warp == 0 && sub == 0 && active) {
@@ -459,9 +576,10 @@ void deal(HeadTensor& t, int64_t rows, int64_t heads, int64_t dim, int num_sms, 
     const int64_t items = rows * t.groups;
     t.items = static_cast<uint32_t>(items);
     int64_t blocks = (items + kHeadWarps - 1) / kHeadWarps;
-    // backward: a bounded number of blocks, each with one row of partial sums
+    // backward: one block an SM and tensor (both tensors' blocks run at once),
+    // each with one row of partial sums
     int64_t most = 1ll << 30;
-    if (persistent) most = 2ll * num_sms < kHeadGradRows ? 2ll * num_sms : kHeadGradRows;
+    if (persistent) most = num_sms < kHeadGradRows ? num_sms : kHeadGradRows;
     t.blocks = static_cast<uint32_t>(blocks < most ? blocks : most);
 }
 
