@@ -15,8 +15,8 @@
 // every head, so the cosines, sines and norm weights of its channels are
 // computed or loaded once a token and stay in registers, and no table of
 // angles is read.  Eight channels are 16 bytes of a 16-bit type; a head of d
-// channels takes d / 8 lanes, and several heads share a pass of the warp when
-// d <= 128.  Pairs are computed two at a time (f32x2): the norm's gradient
+// channels takes d / 8 lanes, and as many heads as fit share a pass of the warp
+// (three of 72 channels).  Pairs are computed two at a time (f32x2): the norm's gradient
 // took 195 us without.
 //
 // Measured (32760 tokens, 40 + 40 heads of 128, bf16, 1.34 GB): rotation 207 us
@@ -88,24 +88,11 @@ __device__ __forceinline__ F2 make_f2(float lo, float hi) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
     return v;
 }
-__device__ __forceinline__ float lo(F2 v) {
-    float a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-    return a;
-}
-__device__ __forceinline__ float hi(F2 v) {
-    float a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-    return b;
-}
+__device__ __forceinline__ float lo(F2 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi(F2 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 __device__ __forceinline__ F2 mul(F2 a, F2 b) {
     F2 v;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-    return v;
-}
-__device__ __forceinline__ F2 add(F2 a, F2 b) {
-    F2 v;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
     return v;
 }
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
@@ -229,16 +216,25 @@ __device__ __forceinline__ void turn(Pairs& p, const F2 (&a)[2], const F2 (&nb)[
     }
 }
 
+// Sum over a head's lanes, in every one of them.  LANES = 0: heads of any
+// number of lanes; `top` is the largest power of two below it.
 template <int LANES>
-__device__ __forceinline__ float head_sum(float v) {
+__device__ __forceinline__ float head_sum(float v, int chunk, int lanes, int top, int head_lane) {
+    if constexpr (LANES > 0) {
 #pragma unroll
-    for (int m = LANES / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
-    return v;
+        for (int m = LANES / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+        return v;
+    } else {
+        for (int m = top; m > 0; m >>= 1) {
+            const float other = __shfl_down_sync(0xFFFFFFFFu, v, m);
+            if (chunk + m < lanes && chunk < m) v += other;
+        }
+        return __shfl_sync(0xFFFFFFFFu, v, head_lane);
+    }
 }
 
 template <typename T, int LANES, bool HALF, int KIND>
 __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) rtlynx_heads_kernel(const __grid_constant__ HeadArgs args) {
-    constexpr int kHeadsPerPass = 32 / LANES;
     // Passes loaded before the first is used, and whether the next ones are
     // loaded before these are computed.  Registers decide: forward, 64 of them
     // leave 32 warps an SM, which hide the latency without looking ahead
@@ -264,8 +260,15 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
     const HeadTensor& t = args.t[keys ? 1 : 0];
     const uint32_t block = blockIdx.x - (keys ? args.t[0].blocks : 0u);
 
-    const int chunk = lane % LANES, sub = lane / LANES;
-    const bool active = chunk * 8 < args.dim;
+    // a head takes `lanes` lanes, a pass of the warp as many heads as fit
+    const int lanes = LANES > 0 ? LANES : args.dim / 8;
+    const int per_pass = 32 / lanes;
+    const int chunk = lane % lanes, sub = lane / lanes;
+    const bool active = LANES > 0 || sub < per_pass;
+    int top = 1;
+    while (LANES == 0 && 2 * top < lanes) top *= 2;
+    if (lanes == 1) top = 0;
+    auto sum_head = [&](float v) { return head_sum<LANES>(v, chunk, lanes, top, lane - chunk); };
     const int rotated = 2 * args.pairs;
     const bool whole = rotated == args.dim;
     // channel offsets of the lane's two runs of four
@@ -341,12 +344,12 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
         const T* x = static_cast<const T*>(t.x) + bi * t.xb + si * t.xs;
         const T* dy = KIND == kNormBackward ? static_cast<const T*>(t.dy) + bi * t.gb + si * t.gs : nullptr;
         T* y = static_cast<T*>(t.y) + bi * t.yb + si * t.ys;
-        const uint32_t first = group * t.passes * kHeadsPerPass;
-        const uint32_t last = min(first + t.passes * kHeadsPerPass, t.heads);
+        const uint32_t first = group * t.passes * per_pass;
+        const uint32_t last = min(first + t.passes * per_pass, t.heads);
         auto fetch = [&](uint32_t h0, Raw<T>(&rx)[kUnroll], Raw<T>(&rg)[kGrads]) {
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const uint32_t h = h0 + u * kHeadsPerPass + sub;
+                const uint32_t h = h0 + u * per_pass + sub;
 #pragma unroll
                 for (int j = 0; j < static_cast<int>(2 * sizeof(T)); ++j) {
                     rx[u].r[j] = 0u;
@@ -360,21 +363,21 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
         };
         Raw<T> rx[kUnroll], rg[kGrads];
         if (kPipe) fetch(first, rx, rg);
-        for (uint32_t h0 = first; h0 < last; h0 += kHeadsPerPass * kUnroll) {
+        for (uint32_t h0 = first; h0 < last; h0 += per_pass * kUnroll) {
             Raw<T> nx[kUnroll], ng[kGrads];
             if (kPipe)
-                fetch(h0 + kHeadsPerPass * kUnroll, nx, ng);
+                fetch(h0 + per_pass * kUnroll, nx, ng);
             else
                 fetch(h0, rx, rg);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {  // heads past the last are zeros, and not stored
-                const uint32_t h = h0 + u * kHeadsPerPass + sub;
+                const uint32_t h = h0 + u * per_pass + sub;
                 Pairs v = unpack<T, HALF>(rx[u]);
                 if constexpr (KIND == kRope) {
                     turn(v, ca, nb, cc, cd, whole, turned);
                 } else {
                     const F2 squares = fma2(v.y[1], v.y[1], fma2(v.x[1], v.x[1], fma2(v.y[0], v.y[0], mul(v.x[0], v.x[0]))));
-                    const float r = rsqrtf(fmaf(head_sum<LANES>(lo(squares) + hi(squares)), inv_dim, args.eps));
+                    const float r = rsqrtf(fmaf(sum_head(lo(squares) + hi(squares)), inv_dim, args.eps));
                     const F2 r2 = make_f2(r, r);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {  // n
@@ -396,7 +399,7 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
                             dot = fma2(g.x[i], v.x[i], dot);
                             dot = fma2(g.y[i], v.y[i], dot);
                         }
-                        const float mean = -head_sum<LANES>(lo(dot) + hi(dot)) * inv_dim;
+                        const float mean = -sum_head(lo(dot) + hi(dot)) * inv_dim;
                         const F2 mean2 = make_f2(mean, mean);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -430,8 +433,8 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-#pragma unroll
-            for (int m = LANES; m < 32; m <<= 1) sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], m);
+            const float own = sum[j];
+            for (int k = 1; k < per_pass; ++k) sum[j] += __shfl_sync(0xFFFFFFFFu, own, (chunk + k * lanes) & 31);
             if (sub == 0) sums[(warp * 32 + chunk) * 8 + j] = sum[j];
         }
         __syncthreads();
@@ -559,13 +562,13 @@ bool ranges_meet(const void* p, Wide np, const void* q, Wide nq) {
 
 int elem_bytes(int dtype) { return dtype == RTLYNX_FP32 ? 4 : 2; }
 
-int lanes_of(int64_t dim) { return dim <= 32 ? 4 : (dim <= 64 ? 8 : (dim <= 128 ? 16 : 32)); }
+int heads_per_pass(int64_t dim) { return static_cast<int>(32 / (dim / 8)); }
 
 // How a tensor's token-heads are dealt to warps.  A warp takes all heads of a
 // token, so that angles are computed once, unless that leaves fewer than
 // about 16 warps an SM: then a token's heads are cut into more, shorter runs.
 void deal(HeadTensor& t, int64_t rows, int64_t heads, int64_t dim, int num_sms, bool persistent) {
-    const int64_t per_pass = 32 / lanes_of(dim);
+    const int64_t per_pass = heads_per_pass(dim);
     const int64_t all = (heads + per_pass - 1) / per_pass;
     const int64_t want = 16ll * num_sms;
     int64_t groups = rows >= want ? 1 : (want + rows - 1) / rows;
@@ -598,11 +601,11 @@ int launch_lanes(const HeadArgs& args, bool half, int kind, cudaStream_t stream)
 
 template <typename T>
 int launch_type(const HeadArgs& args, bool half, int kind, cudaStream_t stream) {
-    switch (lanes_of(args.dim)) {
-        case 4: return launch_lanes<T, 4>(args, half, kind, stream);
-        case 8: return launch_lanes<T, 8>(args, half, kind, stream);
-        case 16: return launch_lanes<T, 16>(args, half, kind, stream);
-        default: return launch_lanes<T, 32>(args, half, kind, stream);
+    switch (args.dim) {
+        case 64: return launch_lanes<T, 8>(args, half, kind, stream);
+        case 128: return launch_lanes<T, 16>(args, half, kind, stream);
+        case 256: return launch_lanes<T, 32>(args, half, kind, stream);
+        default: return launch_lanes<T, 0>(args, half, kind, stream);
     }
 }
 
@@ -725,7 +728,7 @@ int run_heads(int kind, float sin_sign, const Call& call, int64_t B, int64_t S, 
         }
         h.w = call.w[t];
         const int64_t rows = B * S;
-        const int64_t passes = (call.x[t]->heads * lanes_of(D) + 31) / 32;
+        const int64_t passes = (call.x[t]->heads + heads_per_pass(D) - 1) / heads_per_pass(D);
         if (rows * passes > (int64_t(1) << 31)) return RTLYNX_ERR_UNSUPPORTED;  // items fit 32 bits whatever the deal
         deal(h, rows, call.x[t]->heads, D, num_sms, kind == kNormBackward);
         if (call.dw[t])

@@ -105,6 +105,10 @@ CASES = [
     ("fp16", 1, 700, 40, 8, 24, (6, 6, 6), rl.ROPE_INTERLEAVED, "plain"),
     ("bf16", 1, 3000, 9, 1, 64, (20, 44), rl.ROPE_INTERLEAVED, "heads_first"),
     ("bf16", 4, 13, 2, 2, 16, (16,), rl.ROPE_HALF, "broadcast"),
+    ("fp16", 1, 50, 7, 5, 40, (10, 30), rl.ROPE_HALF, "packed"),     # six heads of five lanes a warp pass
+    ("fp32", 2, 31, 8, 4, 80, (16, 32, 32), rl.ROPE_HALF, "plain"),  # three of ten
+    ("bf16", 1, 70, 33, 1, 8, (2, 4), rl.ROPE_INTERLEAVED, "packed"),  # 32 heads of one lane
+    ("bf16", 1, 17, 5, 2, 136, (8, 64, 64), rl.ROPE_INTERLEAVED, "heads_first"),  # one head of 17
 ]
 
 
