@@ -475,6 +475,13 @@ class _HeadsCall:
         self.spec = rope.specs[kind]
         self.handle, self.ctx = _launch_on(self.device, stream)
 
+    def first(self, t):
+        """View of the tensor that the others are checked against."""
+        st, sh = t.stride(), self.shape
+        if st[-1] != 1 and sh[-1] > 1:
+            raise ValueError(f"the channels of a head are contiguous, got strides {st}")
+        return HeadsView(t.data_ptr(), sh[-2], st[0] if len(sh) == 4 else 0, st[-3], st[-2])
+
     def view(self, t, what, keys=False):
         if t is None:
             return None
@@ -488,23 +495,27 @@ class _HeadsCall:
         return w.data_ptr()
 
     def outputs(self, out, q, k):
+        """((queries, view), (keys, view)) of `out`, or of new contiguous tensors."""
+        if out is not None:
+            return (out[0], self.view(out[0], "q_out")), \
+                (None, None) if k is None else (out[1], _heads_view(out[1], k.shape, self.dtype, self.device, "k_out"))
+        return self.new(q), (None, None) if k is None else self.new(k)
+
+    def new(self, like):
         import torch
-        if out is None:
-            plain = torch.contiguous_format
-            out = torch.empty_like(q, memory_format=plain), \
-                None if k is None else torch.empty_like(k, memory_format=plain)
-        return out[0], None if k is None else out[1]
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)
+        row = like.shape[-2] * self.D
+        return t, HeadsView(t.data_ptr(), like.shape[-2], self.S * row, row, self.D)
 
 
 def _run_rope(name, q, k, positions, rope, out, stream):
     c = _HeadsCall(q, k, positions, rope, stream)
     with c.ctx:
-        qo, ko = c.outputs(out, q, k)
-        status = getattr(lib(), name)(
-            c.view(q, "q"), c.view(k, "k", True), c.view(qo, "q_out"), None if ko is None else
-            _heads_view(ko, k.shape, c.dtype, c.device, "k_out"), c.B, c.S, c.D, c.code, c.spec, positions.data_ptr(),
-            *c.strides, c.handle)
-    _check(status, name)
+        (qo, qo_view), (ko, ko_view) = c.outputs(out, q, k)
+        status = getattr(lib(), name)(c.first(q), c.view(k, "k", True), qo_view, ko_view, c.B, c.S, c.D, c.code,
+                                      c.spec, positions.data_ptr(), *c.strides, c.handle)
+    if status:
+        _check(status, name)
     return qo, ko
 
 
@@ -524,12 +535,12 @@ def qk_norm_rope(q, k, w_q, w_k, positions, rope, eps=1e-6, out=None, stream=Non
     """rope() of the heads' RMS norms: (R (w_q q / rms q), R (w_k k / rms k)); w_q, w_k [D] in q's type, or None."""
     c = _HeadsCall(q, k, positions, rope, stream)
     with c.ctx:
-        qo, ko = c.outputs(out, q, k)
-        status = lib().rtlynx_qk_norm_rope(
-            c.view(q, "q"), c.view(k, "k", True), c.weight(w_q, "w_q"), c.weight(w_k, "w_k"), c.view(qo, "q_out"),
-            None if ko is None else _heads_view(ko, k.shape, c.dtype, c.device, "k_out"), c.B, c.S, c.D, c.code, eps,
-            c.spec, positions.data_ptr(), *c.strides, c.handle)
-    _check(status, "rtlynx_qk_norm_rope")
+        (qo, qo_view), (ko, ko_view) = c.outputs(out, q, k)
+        status = lib().rtlynx_qk_norm_rope(c.first(q), c.view(k, "k", True), c.weight(w_q, "w_q"),
+                                           c.weight(w_k, "w_k"), qo_view, ko_view, c.B, c.S, c.D, c.code, eps, c.spec,
+                                           positions.data_ptr(), *c.strides, c.handle)
+    if status:
+        _check(status, "rtlynx_qk_norm_rope")
     return qo, ko
 
 
@@ -543,7 +554,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, w_q, w_k, positions, rope, eps=1
         raise ValueError("dk_out goes with k")
     c = _HeadsCall(q, k, positions, rope, stream)
     with c.ctx:
-        dq, dk = c.outputs(out, q, k)
+        (dq, dq_view), (dk, dk_view) = c.outputs(out, q, k)
         dw_q = torch.empty(c.D, dtype=torch.float32, device=c.device) if weight_grads and w_q is not None else None
         dw_k = torch.empty(c.D, dtype=torch.float32, device=c.device) \
             if weight_grads and w_k is not None and k is not None else None
@@ -552,13 +563,11 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, w_q, w_k, positions, rope, eps=1
             ws_bytes = rtlynx_qk_norm_rope_workspace_size(c.D)
             ws = torch.empty(ws_bytes, dtype=torch.uint8, device=c.device)
 
-        def like_k(t, what):
-            return None if k is None else _heads_view(t, k.shape, c.dtype, c.device, what)
-
+        gk_view = None if k is None else _heads_view(dk_out, k.shape, c.dtype, c.device, "dk_out")
         status = lib().rtlynx_qk_norm_rope_backward(
-            c.view(dq_out, "dq_out"), like_k(dk_out, "dk_out"), c.view(q, "q"), c.view(k, "k", True),
-            c.weight(w_q, "w_q"), c.weight(w_k, "w_k"), c.view(dq, "dq"), like_k(dk, "dk"), _ptr(dw_q), _ptr(dw_k),
-            c.B, c.S, c.D, c.code, eps, c.spec, positions.data_ptr(), *c.strides, _ptr(ws), ws_bytes, c.handle)
+            c.view(dq_out, "dq_out"), gk_view, c.first(q), c.view(k, "k", True), c.weight(w_q, "w_q"),
+            c.weight(w_k, "w_k"), dq_view, dk_view, _ptr(dw_q), _ptr(dw_k), c.B, c.S, c.D, c.code, eps, c.spec,
+            positions.data_ptr(), *c.strides, _ptr(ws), ws_bytes, c.handle)
     _check(status, "rtlynx_qk_norm_rope_backward")
     return dq, dk, dw_q, dw_k
 
