@@ -10,19 +10,20 @@
 //   dx = r (g w - n mean_c(g w n))
 //
 // Every element is read once and written once and needs a handful of
-// operations, so memory bounds it.  A warp owns one token of one tensor and
-// walks over that token's heads: a lane keeps the same eight channels of
-// every head, so the cosines, sines and norm weights of its channels are
-// computed or loaded once a token and stay in registers, and no table of
-// angles is read.  Eight channels are 16 bytes of a 16-bit type; a head of d
-// channels takes d / 8 lanes, and as many heads as fit share a pass of the warp
-// (three of 72 channels).  Pairs are computed two at a time (f32x2): the norm's gradient
-// took 195 us without.
+// operations, so memory bounds it.  A group of lanes owns one token of one
+// tensor and walks over that token's heads, eight channels a lane: a lane keeps
+// the same channels of every head, so the cosines, sines and norm weights of
+// its channels are computed or loaded once a token and stay in registers, and
+// no table of angles is read.  Eight channels are 16 bytes of a 16-bit type; a
+// head of d channels takes d / 8 lanes, and a warp as many tokens as fit (four
+// at 64 channels, two at 128).  (A warp's lanes on several heads of one token
+// instead repeat its angles: 55 us against 23 on 31077 tokens of 12 + 6 heads of
+// 48, and nothing gained with many heads.)  Pairs are computed two at a time
+// (f32x2): the norm's gradient took 195 us without, 179 with.
 //
 // Measured (32760 tokens, 40 + 40 heads of 128, bf16, 1.34 GB): rotation 207 us
-// (6.5 TB/s, the measured copy rate), with the norm 229 us (5.9 TB/s); gradient
-// of both on 16384 tokens (1.01 GB) 179 us (5.6 TB/s).  One warp for a token's
-// queries and keys, with the angles computed once for both, changed nothing.
+// (6.5 TB/s, the measured copy rate), with the norm 220 us (6.1 TB/s); gradient
+// of both on 16384 tokens (1.01 GB) 169 us (6.0 TB/s).
 //
 // Angles: position x frequency / 2 pi in 64 bits, reduced to an eighth of a
 // turn there, so a position of 2^24 loses nothing; sine and cosine of the
@@ -59,8 +60,9 @@ struct HeadTensor {
     const void* w;
     float* part;  // backward: [blocks, dim] partial sums of the weight's gradient
     int64_t xb, xs, xh, gb, gs, gh, yb, ys, yh;  // strides of batch, token, head, in elements
-    uint32_t heads, groups, passes;  // a token's heads are cut into `groups` runs of `passes` warp passes
-    uint32_t items, blocks;
+    uint32_t heads, groups, run;  // a token's heads are cut into `groups` runs of `run`
+    uint32_t rows;                // tokens of all sequences
+    uint32_t items, blocks;       // items: (as many tokens as fit a warp) x groups
 };
 
 struct HeadArgs {
@@ -216,18 +218,19 @@ __device__ __forceinline__ void turn(Pairs& p, const F2 (&a)[2], const F2 (&nb)[
     }
 }
 
-// Sum over a head's lanes, in every one of them.  LANES = 0: heads of any
-// number of lanes; `top` is the largest power of two below it.
+// Sum over a head's lanes, in every one of them.  LANES = 0: heads of up to ten
+// lanes, side by side without a gap; head_lane is the first of them.
 template <int LANES>
-__device__ __forceinline__ float head_sum(float v, int chunk, int lanes, int top, int head_lane) {
+__device__ __forceinline__ float head_sum(float v, int chunk, int lanes, int head_lane) {
     if constexpr (LANES > 0) {
 #pragma unroll
         for (int m = LANES / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
         return v;
     } else {
-        for (int m = top; m > 0; m >>= 1) {
+#pragma unroll
+        for (int m = 8; m > 0; m >>= 1) {
             const float other = __shfl_down_sync(0xFFFFFFFFu, v, m);
-            if (chunk + m < lanes && chunk < m) v += other;
+            if (chunk + m < lanes) v += other;
         }
         return __shfl_sync(0xFFFFFFFFu, v, head_lane);
     }
@@ -235,12 +238,13 @@ __device__ __forceinline__ float head_sum(float v, int chunk, int lanes, int top
 
 template <typename T, int LANES, bool HALF, int KIND>
 __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) rtlynx_heads_kernel(const __grid_constant__ HeadArgs args) {
-    // Passes loaded before the first is used, and whether the next ones are
+    // Heads loaded before the first is used, and whether the next ones are
     // loaded before these are computed.  Registers decide: forward, 64 of them
     // leave 32 warps an SM, which hide the latency without looking ahead
-    // (video workload's norm: 229 us; two passes and looking ahead 235, 80
-    // registers 249); backward, with two tensors read and the weights' sums
-    // kept, 128 and 16 warps, looking ahead (179 us; without 205, two passes 190).
+    // (video workload's norm: 229 us when measured; two heads and looking
+    // ahead 235, 80 registers 249); backward, with two tensors read and the weights' sums
+    // kept, 128 and 16 warps, looking ahead (179 us when
+    // measured; without 205, two heads 190).
     constexpr int kUnroll = 4 / (sizeof(T) == 4 ? 2 : 1);
     constexpr int kGrads = KIND == kNormBackward ? kUnroll : 1;
     constexpr bool kPipe = KIND == kNormBackward;
@@ -255,20 +259,19 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
     }
     __syncthreads();
     grid_dependency_wait();
+    launch_dependents();
 
     const bool keys = blockIdx.x >= args.t[0].blocks;
     const HeadTensor& t = args.t[keys ? 1 : 0];
     const uint32_t block = blockIdx.x - (keys ? args.t[0].blocks : 0u);
 
-    // a head takes `lanes` lanes, a pass of the warp as many heads as fit
+    // a head takes `lanes` lanes (some of them idle where they are LANES), a
+    // pass of the warp as many heads as fit
     const int lanes = LANES > 0 ? LANES : args.dim / 8;
     const int per_pass = 32 / lanes;
     const int chunk = lane % lanes, sub = lane / lanes;
-    const bool active = LANES > 0 || sub < per_pass;
-    int top = 1;
-    while (LANES == 0 && 2 * top < lanes) top *= 2;
-    if (lanes == 1) top = 0;
-    auto sum_head = [&](float v) { return head_sum<LANES>(v, chunk, lanes, top, lane - chunk); };
+    const bool active = LANES > 0 ? 8 * chunk < args.dim : sub < per_pass;
+    auto sum_head = [&](float v) { return head_sum<LANES>(v, chunk, lanes, lane - chunk); };
     const int rotated = 2 * args.pairs;
     const bool whole = rotated == args.dim;
     // channel offsets of the lane's two runs of four
@@ -292,8 +295,32 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
     const float inv_dim = 1.0f / static_cast<float>(args.dim);
 
     for (uint32_t item = block * kHeadWarps + warp; item < t.items; item += t.blocks * kHeadWarps) {
-        const uint32_t token = item / t.groups, group = item - token * t.groups;
+        const uint32_t slot = item / t.groups, group = item - slot * t.groups;
+        const uint32_t token = slot * per_pass + sub;
+        const bool live = active && token < t.rows;
         const uint32_t bi = token / args.tokens, si = token - bi * args.tokens;
+        const T* x = static_cast<const T*>(t.x) + bi * t.xb + si * t.xs;
+        const T* dy = KIND == kNormBackward ? static_cast<const T*>(t.dy) + bi * t.gb + si * t.gs : nullptr;
+        T* y = static_cast<T*>(t.y) + bi * t.yb + si * t.ys;
+        const uint32_t first = group * t.run;
+        const uint32_t last = min(first + t.run, t.heads);
+        auto fetch = [&](uint32_t h0, Raw<T>(&rx)[kUnroll], Raw<T>(&rg)[kGrads]) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const uint32_t h = h0 + u;
+#pragma unroll
+                for (int j = 0; j < static_cast<int>(2 * sizeof(T)); ++j) {
+                    rx[u].r[j] = 0u;
+                    if (KIND == kNormBackward) rg[u % kGrads].r[j] = 0u;
+                }
+                if (live && h < last) {
+                    load8<T, HALF>(x + h * t.xh, a, b, rx[u]);
+                    if constexpr (KIND == kNormBackward) load8<T, HALF>(dy + h * t.gh, a, b, rg[u]);
+                }
+            }
+        };
+        Raw<T> rx[kUnroll], rg[kGrads];
+        fetch(first, rx, rg);  // on their way while the angles are computed
 
         float c[4], s[4];
         uint32_t turned = 0;
@@ -302,7 +329,7 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
             c[j] = 1.0f;
             s[j] = 0.0f;
             const int i = 4 * chunk + j;
-            if (i < args.pairs) {
+            if (live && i < args.pairs) {
                 const int64_t at = bi * args.pb + si * args.ps + axis[i] * args.pa;
                 double p;
                 if (args.pos_type == RTLYNX_POS_INT32)
@@ -341,37 +368,12 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
             }
         }
 
-        const T* x = static_cast<const T*>(t.x) + bi * t.xb + si * t.xs;
-        const T* dy = KIND == kNormBackward ? static_cast<const T*>(t.dy) + bi * t.gb + si * t.gs : nullptr;
-        T* y = static_cast<T*>(t.y) + bi * t.yb + si * t.ys;
-        const uint32_t first = group * t.passes * per_pass;
-        const uint32_t last = min(first + t.passes * per_pass, t.heads);
-        auto fetch = [&](uint32_t h0, Raw<T>(&rx)[kUnroll], Raw<T>(&rg)[kGrads]) {
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const uint32_t h = h0 + u * per_pass + sub;
-#pragma unroll
-                for (int j = 0; j < static_cast<int>(2 * sizeof(T)); ++j) {
-                    rx[u].r[j] = 0u;
-                    if (KIND == kNormBackward) rg[u % kGrads].r[j] = 0u;
-                }
-                if (active && h < last) {
-                    load8<T, HALF>(x + h * t.xh, a, b, rx[u]);
-                    if constexpr (KIND == kNormBackward) load8<T, HALF>(dy + h * t.gh, a, b, rg[u]);
-                }
-            }
-        };
-        Raw<T> rx[kUnroll], rg[kGrads];
-        if (kPipe) fetch(first, rx, rg);
-        for (uint32_t h0 = first; h0 < last; h0 += per_pass * kUnroll) {
+        for (uint32_t h0 = first; h0 < last; h0 += kUnroll) {
             Raw<T> nx[kUnroll], ng[kGrads];
-            if (kPipe)
-                fetch(h0 + per_pass * kUnroll, nx, ng);
-            else
-                fetch(h0, rx, rg);
+            if (kPipe) fetch(h0 + kUnroll, nx, ng);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {  // heads past the last are zeros, and not stored
-                const uint32_t h = h0 + u * per_pass + sub;
+                const uint32_t h = h0 + u;
                 Pairs v = unpack<T, HALF>(rx[u]);
                 if constexpr (KIND == kRope) {
                     turn(v, ca, nb, cc, cd, whole, turned);
@@ -408,13 +410,15 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
                         }
                     }
                 }
-                if (active && h < last) store8<T, HALF>(y + h * t.yh, a, b, pack<T, HALF>(v));
+                if (live && h < last) store8<T, HALF>(y + h * t.yh, a, b, pack<T, HALF>(v));
             }
             if (kPipe) {
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) rx[u] = nx[u];
 #pragma unroll
                 for (int u = 0; u < kGrads; ++u) rg[u] = ng[u];
+            } else {
+                fetch(h0 + kUnroll, rx, rg);
             }
         }
     }
@@ -562,23 +566,33 @@ bool ranges_meet(const void* p, Wide np, const void* q, Wide nq) {
 
 int elem_bytes(int dtype) { return dtype == RTLYNX_FP32 ? 4 : 2; }
 
-int heads_per_pass(int64_t dim) { return static_cast<int>(32 / (dim / 8)); }
+// Lanes that a head takes: as many as it has eights of channels where that lets
+// more heads into a warp pass than the next power of two, whose sums need
+// fewer steps.
+int lanes_of(int64_t dim) {
+    const int exact = static_cast<int>(dim / 8);
+    int power = 8;
+    while (power < exact) power *= 2;
+    return 32 / exact > 32 / power ? exact : power;
+}
+int heads_per_pass(int64_t dim) { return 32 / lanes_of(dim); }
 
-// How a tensor's token-heads are dealt to warps.  A warp takes all heads of a
-// token, so that angles are computed once, unless that leaves fewer than
-// about 16 warps an SM: then a token's heads are cut into more, shorter runs.
+// How a tensor's token-heads are dealt to warps.  A group of lanes takes all
+// heads of its token, so that angles are computed once, unless that leaves
+// fewer than about 16 warps an SM: then the heads are cut into shorter runs.
 void deal(HeadTensor& t, int64_t rows, int64_t heads, int64_t dim, int num_sms, bool persistent) {
     const int64_t per_pass = heads_per_pass(dim);
-    const int64_t all = (heads + per_pass - 1) / per_pass;
+    const int64_t slots = (rows + per_pass - 1) / per_pass;
     const int64_t want = 16ll * num_sms;
-    int64_t groups = rows >= want ? 1 : (want + rows - 1) / rows;
-    if (groups > all) groups = all;
-    t.passes = static_cast<uint32_t>((all + groups - 1) / groups);
-    t.groups = static_cast<uint32_t>((all + t.passes - 1) / t.passes);
+    int64_t groups = slots >= want ? 1 : (want + slots - 1) / slots;
+    if (groups > heads) groups = heads;
+    t.run = static_cast<uint32_t>((heads + groups - 1) / groups);
+    t.groups = static_cast<uint32_t>((heads + t.run - 1) / t.run);
     t.heads = static_cast<uint32_t>(heads);
-    const int64_t items = rows * t.groups;
+    t.rows = static_cast<uint32_t>(rows);
+    const int64_t items = slots * t.groups;
     t.items = static_cast<uint32_t>(items);
-    int64_t blocks = (items + kHeadWarps - 1) / kHeadWarps;
+    const int64_t blocks = (items + kHeadWarps - 1) / kHeadWarps;
     // backward: one block an SM and tensor (both tensors' blocks run at once),
     // each with one row of partial sums
     int64_t most = 1ll << 30;
@@ -601,10 +615,10 @@ int launch_lanes(const HeadArgs& args, bool half, int kind, cudaStream_t stream)
 
 template <typename T>
 int launch_type(const HeadArgs& args, bool half, int kind, cudaStream_t stream) {
-    switch (args.dim) {
-        case 64: return launch_lanes<T, 8>(args, half, kind, stream);
-        case 128: return launch_lanes<T, 16>(args, half, kind, stream);
-        case 256: return launch_lanes<T, 32>(args, half, kind, stream);
+    switch (lanes_of(args.dim)) {
+        case 8: return launch_lanes<T, 8>(args, half, kind, stream);
+        case 16: return launch_lanes<T, 16>(args, half, kind, stream);
+        case 32: return launch_lanes<T, 32>(args, half, kind, stream);
         default: return launch_lanes<T, 0>(args, half, kind, stream);
     }
 }
@@ -728,8 +742,7 @@ int run_heads(int kind, float sin_sign, const Call& call, int64_t B, int64_t S, 
         }
         h.w = call.w[t];
         const int64_t rows = B * S;
-        const int64_t passes = (call.x[t]->heads + heads_per_pass(D) - 1) / heads_per_pass(D);
-        if (rows * passes > (int64_t(1) << 31)) return RTLYNX_ERR_UNSUPPORTED;  // items fit 32 bits whatever the deal
+        if (rows * call.x[t]->heads > (int64_t(1) << 31)) return RTLYNX_ERR_UNSUPPORTED;  // items fit 32 bits
         deal(h, rows, call.x[t]->heads, D, num_sms, kind == kNormBackward);
         if (call.dw[t])
             h.part = static_cast<float*>(workspace) + static_cast<size_t>(t) * kHeadGradRows * D;
