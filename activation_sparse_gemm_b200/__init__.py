@@ -49,7 +49,7 @@ ABI_SYMBOLS = (
     "rtlynx_sparsify_debug", "rtlynx_linear_host", "rtlynx_mlp_block", "rtlynx_linear_noalloc",
     "rtlynx_kernel_launches", "rtlynx_schedule_info",
     "rtlynx_quantize_weight_fp8", "rtlynx_linear_fp8", "rtlynx_linear_fp8_events", "rtlynx_sparsify_fp8_debug",
-    "rtlynx_gated_mlp_block", "rtlynx_gated_mlp_backward_workspace_size", "rtlynx_gated_mlp_backward",
+    "rtlynx_gated_mlp_block", "rtlynx_gated_mlp_block_workspace_size", "rtlynx_gated_mlp_backward_workspace_size", "rtlynx_gated_mlp_backward",
     "rtlynx_rope", "rtlynx_rope_backward", "rtlynx_qk_norm_rope", "rtlynx_qk_norm_rope_workspace_size",
     "rtlynx_qk_norm_rope_backward",
     "rtlynx_wait_selftest", "rtlynx_stream_status", "rtlynx_status_string", "rtlynx_release",
@@ -130,8 +130,10 @@ def lib() -> ctypes.CDLL:
         L.rtlynx_kernel_launches.restype = i
         L.rtlynx_schedule_info.argtypes = [i64, i64, i64, i64, i, ctypes.POINTER(Schedule)]
         L.rtlynx_schedule_info.restype = i
-        L.rtlynx_gated_mlp_block.argtypes = [p] * 10 + [i64, i64, i64, i64, i, i, p]
+        L.rtlynx_gated_mlp_block.argtypes = [p] * 10 + [i64, i64, i64, i64, i, i, p, ctypes.c_size_t, p]
         L.rtlynx_gated_mlp_block.restype = i
+        L.rtlynx_gated_mlp_block_workspace_size.argtypes = [i64, i64, i64, i]
+        L.rtlynx_gated_mlp_block_workspace_size.restype = ctypes.c_size_t
         L.rtlynx_gated_mlp_backward_workspace_size.argtypes = [i64, i64, i64]
         L.rtlynx_gated_mlp_backward_workspace_size.restype = ctypes.c_size_t
         L.rtlynx_gated_mlp_backward.argtypes = [p] * 12 + [i64, i64, i64, i, p, ctypes.c_size_t, p]
@@ -275,12 +277,17 @@ def rtlynx_sparsify_fp8_debug(X, M, D_in, codes, meta, qx, stream=None) -> int:
                                                   _stream(stream)), "rtlynx_sparsify_fp8_debug")
 
 
-def rtlynx_gated_mlp_block(X, W_gate, W_up, W_down, LA_down, LB_down, G, U, H, Y, M, D, D_ff, R, act=ACT_SILU,
-                           mode_down=MODE_DENSE_SKIP, stream=None) -> int:
+def rtlynx_gated_mlp_block_workspace_size(M, D, D_ff, mode_down=MODE_DENSE_SKIP) -> int:
+    return int(lib().rtlynx_gated_mlp_block_workspace_size(M, D, D_ff, mode_down))
+
+
+def rtlynx_gated_mlp_block(X, W_gate, W_up, W_down, LA_down, LB_down, G, U, H, Y, M, D, D_ff, R, act, mode_down,
+                           workspace, ws_bytes, stream=None) -> int:
     """H = act(X W_gate^T) * (X W_up^T) [M, D_ff], Y = layer_down(H) [M, D]; see include/rtlynx.h."""
     return _check(lib().rtlynx_gated_mlp_block(_ptr(X), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _ptr(LA_down),
                                                _ptr(LB_down), _ptr(G), _ptr(U), _ptr(H), _ptr(Y), M, D, D_ff, R, act,
-                                               mode_down, _stream(stream)), "rtlynx_gated_mlp_block")
+                                               mode_down, _ptr(workspace), ws_bytes, _stream(stream)),
+                  "rtlynx_gated_mlp_block")
 
 
 def rtlynx_gated_mlp_backward_workspace_size(M, D, D_ff) -> int:
@@ -611,8 +618,10 @@ def gated_mlp(X, W_gate, W_up, W_down, act=ACT_SILU, L_A=None, L_B=None, mode_do
             Y, y = out, _matrix(out, M, D, device, "out")
         H = torch.empty((M, F), dtype=X.dtype, device=device)
         G, U = (torch.empty_like(H), torch.empty_like(H)) if save else (None, None)
+        ws_bytes = lib().rtlynx_gated_mlp_block_workspace_size(M, D, F, mode_down)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
         status = lib().rtlynx_gated_mlp_block(*at, la, lb, _ptr(G), _ptr(U), H.data_ptr(), y, M, D, F, R, act,
-                                              mode_down, handle)
+                                              mode_down, _ptr(ws), ws_bytes, handle)
     _check(status, "rtlynx_gated_mlp_block")
     return (Y, (G, U, H)) if save else Y
 

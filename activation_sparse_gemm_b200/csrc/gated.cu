@@ -40,14 +40,19 @@ namespace rtlynx {
 namespace {
 
 constexpr uint32_t kTmemColumns = 512;
-constexpr int kTile = 256;                      // rows and accumulator columns of a tile
+constexpr int kTile = 256;                      // rows of a tile, and accumulator columns unless narrow
 constexpr int kHalf = 128;                      // one CTA's share of either operand
+constexpr int kNarrow = 128;                    // accumulator columns of a narrow tile
 constexpr int kOperandBytes = kHalf * 64 * 2;   // 128 x 64 values
 constexpr int kStageBytes = 2 * kOperandBytes;  // A and B
 constexpr int kStages = 6;
-constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 1024;
+constexpr int kEpiWarps = 8;                    // two on each quadrant of tensor-memory lanes, half of the columns each
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kPieceBytes = 32 * 32 * 2;        // 32 rows x 32 columns on their way out
+constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * 2 * kPieceBytes + 1024 + 1024;
 constexpr int kMaxProblems = 4;
-constexpr int kMaxMaps = 12;
+constexpr int kMaxMaps = 16;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 enum Epilogue { kStore = 0, kGatedForward = 1, kGatedBackward = 2 };
 
@@ -60,7 +65,8 @@ struct Problem {
     int a0, b0, a1, b1;
     int a_mn, b_mn;             // operand is MN-major
     int rows, cols;             // of the output
-    uint16_t* out[3];           // forward: H, G, U (G, U may be null); backward: dG, dU; store: the output
+    int out[3];                 // maps of the outputs; forward: H, G, U (G, U may be -1); backward: dG, dU
+    uint16_t* sum_out;          // split > 1: the output of the summing kernel
     const uint16_t* in[2];      // backward: G, U
     float* part;                // split > 1: fp32 partial tiles
 };
@@ -151,6 +157,17 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
                       pack_bf16x2(v[6], v[7]));
 }
 
+// 32 accumulator columns, rounded.
+__device__ __forceinline__ void pack32(const uint32_t (&r)[32], uint4 (&v)[4]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[8 * q + j]);
+        v[q] = pack8(f);
+    }
+}
+
 __device__ __forceinline__ void unpack8(uint4 u, float* v) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -160,22 +177,17 @@ __device__ __forceinline__ void unpack8(uint4 u, float* v) {
     }
 }
 
-// Epilogue warps: four, or eight where the epilogue's own memory traffic would
-// otherwise outlast the main loop it overlaps; then two warps share a
-// quadrant of tensor-memory lanes and take half of the columns each.
-template <int EPI>
-struct Shape {
-    static constexpr int kEpiWarps = EPI == kStore ? 4 : 8;
-    static constexpr int kThreads = 64 + 32 * kEpiWarps;
-};
-
-template <int EPI, int ACT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads, 1)
+// TN: accumulator columns of a tile, half of them from either CTA's rows of B.
+template <int EPI, int ACT, int TN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     rtlynx_gated_gemm_kernel(const __grid_constant__ GatedArgs args) {
-    constexpr int kEpiWarps = Shape<EPI>::kEpiWarps;
+    constexpr int kColumns = TN / 2;  // rows of B a CTA holds
+    constexpr uint32_t kStageLoads = kOperandBytes + kColumns * 64 * 2;
+    static_assert(EPI == kGatedForward || TN == kTile, "only the forward epilogue has narrow tiles");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+    uint8_t* pieces = smem + kStages * kStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(pieces + kEpiWarps * 2 * kPieceBytes);
     uint64_t* empty = full + kStages;
     uint64_t* acc_full = empty + kStages;  // [2]
     uint64_t* acc_empty = acc_full + 2;    // [2], used in the leader only
@@ -213,6 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
     grid_dependency_wait();
+    launch_dependents();  // the next kernel's setup may overlap this one
 
     Unit w;
     if (warp == 0) {
@@ -236,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
                 const uint32_t dst = smem0 + static_cast<uint32_t>(stage * kStageBytes);
                 const uint32_t bar = full0 + static_cast<uint32_t>(stage) * 8u;
                 if (elect_one()) {
-                    if (leader) mbar_arrive_expect_tx(&full[stage], 2u * kStageBytes);
+                    if (leader) mbar_arrive_expect_tx(&full[stage], 2u * kStageLoads);
                     load_operand<A_MN>(dst, ma, bar, k, row0);
                     load_operand<B_MN>(dst + kOperandBytes, mb, bar, k, col0);
                 }
@@ -249,14 +262,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
         for (int i = 0; ok && unit_at(i, pair, num_pairs, args, w); ++i) {
             const Problem& p = args.p[w.problem];
             const int row0 = w.mp * kTile + static_cast<int>(rank) * kHalf;
-            const int col0 = EPI == kGatedForward ? w.nt * kHalf : w.nt * kTile + static_cast<int>(rank) * kHalf;
+            const int col0 = EPI == kGatedForward ? w.nt * kColumns : w.nt * kTile + static_cast<int>(rank) * kHalf;
             // one run of stages for each operand pair
             for (int seg = 0; seg < 2 && ok; ++seg) {
                 const int begin = seg ? max(w.kb, p.k0) : w.kb, end = seg ? w.ke : min(w.ke, p.k0);
                 const CUtensorMap* ma = &args.maps[seg ? p.a1 : p.a0];
                 const CUtensorMap* mb = &args.maps[(seg ? p.b1 : p.b0) + (EPI == kGatedForward ? static_cast<int>(rank) : 0)];
                 const int k = (begin - (seg ? p.k0 : 0)) * 64;
-                if (EPI == kGatedForward) {
+                if (EPI == kGatedForward || (EPI == kStore && !p.b_mn)) {
                     fetch(KMajor(), KMajor(), ma, mb, k, end - begin, row0, col0);
                 } else if (EPI == kGatedBackward || !p.a_mn) {
                     fetch(KMajor(), MnMajor(), ma, mb, k, end - begin, row0, col0);
@@ -292,7 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
             // and uniform values
             auto issue = [&](auto a_major, auto b_major, uint32_t d, int stages) {
                 constexpr bool A_MN = decltype(a_major)::value, B_MN = decltype(b_major)::value;
-                constexpr uint32_t idesc = make_idesc_bf16(kTile, kTile, false) | (A_MN ? 1u << 15 : 0u) |
+                constexpr uint32_t idesc = make_idesc_bf16(kTile, TN, false) | (A_MN ? 1u << 15 : 0u) |
                                            (B_MN ? 1u << 16 : 0u);
                 // MN-major: 64-value blocks 8 KB apart, groups of eight K rows 1 KB apart
                 const uint64_t desc_a = make_sdesc(smem0, A_MN ? kOperandBytes / 2 : 16, 1024, kSw128);
@@ -328,8 +341,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
                 const uint32_t use = static_cast<uint32_t>(local >> 1);
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_empty[buf], (use & 1u) ^ 1u, err))) break;
                 tc_fence_after();
-                const uint32_t d = tmem_base + static_cast<uint32_t>(buf * kTile);
-                if (EPI == kGatedForward) {
+                const uint32_t d = tmem_base + static_cast<uint32_t>(buf * TN);
+                if (EPI == kGatedForward || (EPI == kStore && !p.b_mn)) {
                     issue(KMajor(), KMajor(), d, w.ke - w.kb);
                 } else if (EPI == kGatedBackward || !p.a_mn) {
                     issue(KMajor(), MnMajor(), d, w.ke - w.kb);
@@ -348,43 +361,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
         const int quad = warp & 3;          // tensor-memory lane quadrant of this warp
         const int part = (warp - 2) >> 2;   // which share of the columns
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+        // A lane has 32 columns of its own row: they go out as 32 x 32 pieces
+        // through shared memory (64B swizzle) and TMA, which clips the ragged
+        // edges.  Stored straight from the lanes, 16 bytes to each of 32 rows at
+        // a time, outputs with a short K take twice as long.
+        uint8_t* piece = pieces + (warp - 2) * 2 * kPieceBytes;
+        int turn = 0;
+        auto put = [&](int map, const uint4 (&v)[4], int col, int row) {
+            uint8_t* dst = piece + turn * kPieceBytes;
+            if (lane == 0) bulk_wait_group_read<1>();  // the store that last used dst has read it
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = v[q];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(&args.maps[map], dst, col, row);
+                bulk_commit_group();
+            }
+            turn ^= 1;
+        };
         for (int local = 0; unit_at(local, pair, num_pairs, args, w); ++local) {
             const Problem& p = args.p[w.problem];
             const int buf = local & 1;
             const uint32_t use = static_cast<uint32_t>(local >> 1);
             const int row_in_cta = quad * 32 + lane;
-            const int row = w.mp * kTile + static_cast<int>(rank) * kHalf + row_in_cta;
-            const bool row_ok = row < p.rows;
-            const size_t row_at = static_cast<size_t>(row) * p.cols;
-            const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * kTile) + lane_addr;
+            const int row0 = w.mp * kTile + static_cast<int>(rank) * kHalf + quad * 32;  // of the warp
+            const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * TN) + lane_addr;
             if (!whole_warp_wait(&acc_full[buf], use & 1u, err)) break;
             tc_fence_after();
             if constexpr (EPI == kGatedForward) {
-                constexpr int kCols = kHalf / (kEpiWarps / 4);
+                constexpr int kCols = kColumns / (kEpiWarps / 4);
                 const int c0 = part * kCols;
 #pragma unroll 1
                 for (int c = c0; c < c0 + kCols; c += 32) {
+                    const int col = w.nt * kColumns + c;
+                    if (row0 >= p.rows || col >= p.cols) break;  // the same in the whole warp
                     uint32_t g[32], v[32];
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), g);
-                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(kHalf + c), v);
+                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(kColumns + c), v);
                     tmem_ld_wait();
+                    uint4 packed[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int col = w.nt * kHalf + c + 8 * q;
-                        float gf[8], uf[8], hf[8];
+                        float h[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            gf[j] = __uint_as_float(g[8 * q + j]);
-                            uf[j] = __uint_as_float(v[8 * q + j]);
-                            hf[j] = act_value<ACT>(gf[j]) * uf[j];
-                        }
-                        if (row_ok && col < p.cols) {
-                            *reinterpret_cast<uint4*>(p.out[0] + row_at + col) = pack8(hf);
-                            if (p.out[1]) {
-                                *reinterpret_cast<uint4*>(p.out[1] + row_at + col) = pack8(gf);
-                                *reinterpret_cast<uint4*>(p.out[2] + row_at + col) = pack8(uf);
-                            }
-                        }
+                        for (int j = 0; j < 8; ++j)
+                            h[j] = act_value<ACT>(__uint_as_float(g[8 * q + j])) * __uint_as_float(v[8 * q + j]);
+                        packed[q] = pack8(h);
+                    }
+                    put(p.out[0], packed, col, row0);
+                    if (p.out[1] >= 0) {
+                        pack32(g, packed);
+                        put(p.out[1], packed, col, row0);
+                        pack32(v, packed);
+                        put(p.out[2], packed, col, row0);
                     }
                 }
             } else if constexpr (EPI == kGatedBackward) {
@@ -394,13 +426,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
                 for (int c = c0; c < c0 + kCols; c += 32) {
                     uint32_t r[32];
                     uint4 gp[4], up[4];
-                    const int col0 = w.nt * kTile + c;
+                    const int col0 = w.nt * kTile + c, row = row0 + lane;
+                    if (row0 >= p.rows || col0 >= p.cols) break;  // the same in the whole warp
+                    const size_t at = static_cast<size_t>(row) * p.cols + col0;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         gp[q] = up[q] = make_uint4(0, 0, 0, 0);
-                        if (row_ok && col0 + 8 * q < p.cols) {
-                            gp[q] = __ldg(reinterpret_cast<const uint4*>(p.in[0] + row_at + col0 + 8 * q));
-                            up[q] = __ldg(reinterpret_cast<const uint4*>(p.in[1] + row_at + col0 + 8 * q));
+                        if (row < p.rows && col0 + 8 * q < p.cols) {
+                            gp[q] = __ldg(reinterpret_cast<const uint4*>(p.in[0] + at + 8 * q));
+                            up[q] = __ldg(reinterpret_cast<const uint4*>(p.in[1] + at + 8 * q));
                         }
                     }
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), r);
@@ -418,17 +452,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
                             gf[j] = dh * uf[j] * slope;
                             uf[j] = dh * value;
                         }
-                        if (row_ok && col0 + 8 * q < p.cols) {
-                            *reinterpret_cast<uint4*>(p.out[0] + row_at + col0 + 8 * q) = pack8(gf);
-                            *reinterpret_cast<uint4*>(p.out[1] + row_at + col0 + 8 * q) = pack8(uf);
-                        }
+                        gp[q] = pack8(gf);
+                        up[q] = pack8(uf);
                     }
+                    put(p.out[0], gp, col0, row0);
+                    put(p.out[1], up, col0, row0);
                 }
             } else if (p.split > 1) {
                 // this CTA's half of the fp32 partial: [column / 4][row][4]
                 float* dst = p.part + (static_cast<size_t>(w.index) * 2 + rank) * (kHalf * kTile);
+                constexpr int kCols = kTile / (kEpiWarps / 4);
 #pragma unroll 1
-                for (int c = 0; c < kTile; c += 32) {
+                for (int c = part * kCols; c < (part + 1) * kCols; c += 32) {
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), r);
                     tmem_ld_wait();
@@ -438,26 +473,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
                             make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
                 }
             } else {
+                constexpr int kCols = kTile / (kEpiWarps / 4);
 #pragma unroll 1
-                for (int c = 0; c < kTile; c += 32) {
+                for (int c = part * kCols; c < (part + 1) * kCols; c += 32) {
+                    const int col = w.nt * kTile + c;
+                    if (row0 >= p.rows || col >= p.cols) break;  // the same in the whole warp
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), r);
                     tmem_ld_wait();
-                    const int col0 = w.nt * kTile + c;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float f[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[8 * q + j]);
-                        if (row_ok && col0 + 8 * q < p.cols)
-                            *reinterpret_cast<uint4*>(p.out[0] + row_at + col0 + 8 * q) = pack8(f);
-                    }
+                    uint4 packed[4];
+                    pack32(r, packed);
+                    put(p.out[0], packed, col, row0);
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
         }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
     }
 
     __syncwarp();  // reconverge the role warps before the cluster barrier
@@ -481,6 +515,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<EPI>::kThreads
 // 256 threads = 2 column octets x 128 rows.
 __global__ void __launch_bounds__(256) rtlynx_gated_sum_parts_kernel(const __grid_constant__ Problem p) {
     grid_dependency_wait();
+    launch_dependents();
     const int tile = blockIdx.x >> 1, rank = blockIdx.x & 1;
     const int row_in_cta = threadIdx.x & 127, octet = blockIdx.y * 2 + (threadIdx.x >> 7);
     const int per_group = p.m_pairs * p.group_n;
@@ -498,19 +533,23 @@ __global__ void __launch_bounds__(256) rtlynx_gated_sum_parts_kernel(const __gri
         sum[0] += a.x, sum[1] += a.y, sum[2] += a.z, sum[3] += a.w;
         sum[4] += b.x, sum[5] += b.y, sum[6] += b.z, sum[7] += b.w;
     }
-    *reinterpret_cast<uint4*>(p.out[0] + static_cast<size_t>(row) * p.cols + col) = pack8(sum);
+    *reinterpret_cast<uint4*>(p.sum_out + static_cast<size_t>(row) * p.cols + col) = pack8(sum);
 }
 
 // ---------------------------------------------------------------- host side
-template <int EPI, int ACT>
+template <int EPI, int ACT, int TN = kTile>
 int launch_gated(const GatedArgs& args, int num_sms, cudaStream_t stream) {
-    auto kernel = rtlynx_gated_gemm_kernel<EPI, ACT>;
+    auto kernel = rtlynx_gated_gemm_kernel<EPI, ACT, TN>;
     static std::atomic<uint64_t> smem_set{0};
     const int e = allow_max_dynamic_smem(kernel, smem_set);
     if (e) return e;
     const int most = num_sms / 2;
     const int pairs = args.units < most ? args.units : most;
-    return launch_dependent(kernel, dim3(2 * pairs), dim3(Shape<EPI>::kThreads), kSmemBytes, stream, args);
+    return launch_dependent(kernel, dim3(2 * pairs), dim3(kThreads), kSmemBytes, stream, args);
+}
+
+int launch_sum_parts(const Problem& p, cudaStream_t stream) {
+    return launch_dependent(rtlynx_gated_sum_parts_kernel, dim3(p.m_pairs * p.n_tiles * 2, 16), dim3(256), 0, stream, p);
 }
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
@@ -533,9 +572,17 @@ struct Maps {
     int count = 0;
     bool ok = true;
     // a [rows, cols] bf16 matrix read in boxes of 64 contiguous values x box_rows
-    int add(const void* base, int64_t rows, int64_t cols, bool mn) {
+    int add(const void* base, int64_t rows, int64_t cols, bool mn, int box_rows = kHalf) {
         if (encode_tmap_uncached(&args.maps[count], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, cols * 2, 64,
-                                 mn ? 64 : kHalf, CU_TENSOR_MAP_SWIZZLE_128B))
+                                 mn ? 64 : box_rows, CU_TENSOR_MAP_SWIZZLE_128B))
+            ok = false;
+        return count++;
+    }
+    // a [rows, cols] bf16 output, written in 32 x 32 pieces
+    int out(void* base, int64_t rows, int64_t cols) {
+        if (!base) return -1;
+        if (encode_tmap_uncached(&args.maps[count], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, cols * 2, 32, 32,
+                                 CU_TENSOR_MAP_SWIZZLE_64B))
             ok = false;
         return count++;
     }
@@ -578,22 +625,40 @@ bool ranges_ok(const Range* in, int n_in, const Range* out, int n_out) {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+constexpr int kAssumedPairs = 74;  // sizes the workspace; a GPU with fewer pairs splits less
+
 // Stages' worth of time that a unit costs beside its stages (filling the
 // pipeline, its share of the epilogue).
 constexpr int kUnitCost = 8;
 
-// Most parts a dX tile is cut into along K = 2 D_ff: its tiles are few and long
-// when there are few tokens, and then each CTA pair gets at most one part, of at
-// least eight stages.
-int dx_most_parts(int64_t M, int64_t D, int64_t F, int pairs) {
-    const int64_t tiles = static_cast<int64_t>(ceil_div(M, kTile)) * ceil_div(D, kTile);
-    const int64_t stages = 2 * ceil_div(F, 64);
+// Most parts that the tiles of a [rows, cols] product are cut into along its
+// `stages` of K: where tiles are fewer than CTA pairs each pair gets at most
+// one part, of at least `least` stages.
+int most_parts(int64_t rows, int64_t cols, int64_t stages, int pairs, int least) {
+    const int64_t tiles = static_cast<int64_t>(ceil_div(rows, kTile)) * ceil_div(cols, kTile);
     int64_t split = pairs / tiles;
-    if (split > stages / 8) split = stages / 8;
+    if (split > stages / least) split = stages / least;
     return static_cast<int>(split < 1 ? 1 : (split > 16 ? 16 : split));
 }
 
-constexpr int kAssumedPairs = 74;  // sizes the workspace; a GPU with fewer pairs splits less
+size_t parts_bytes(int64_t rows, int64_t cols, int split) {
+    const size_t tiles = static_cast<size_t>(ceil_div(rows, kTile)) * ceil_div(cols, kTile);
+    return split > 1 ? tiles * split * kTile * kTile * sizeof(float) : 0;
+}
+
+// Y = H Wd^T of the forward call.
+#ifndef DOWN_LEAST
+#define DOWN_LEAST 16
+#endif
+int down_parts(int64_t M, int64_t D, int64_t F, int pairs) {
+    return most_parts(M, D, ceil_div(F, 64), pairs < kAssumedPairs ? pairs : kAssumedPairs, DOWN_LEAST);
+}
+
+// dX, K = 2 D_ff
+int dx_most_parts(int64_t M, int64_t D, int64_t F, int pairs) {
+    return most_parts(M, D, 2 * ceil_div(F, 64), pairs < kAssumedPairs ? pairs : kAssumedPairs, 8);
+}
+
 
 struct BackwardLayout {
     size_t dg, du, part, total;
@@ -604,9 +669,7 @@ BackwardLayout backward_layout(int64_t M, int64_t D, int64_t F) {
     l.dg = 0;
     l.du = align256(static_cast<size_t>(M) * F * 2);
     l.part = 2 * l.du;
-    const int split = dx_most_parts(M, D, F, kAssumedPairs);
-    const size_t units = static_cast<size_t>(ceil_div(M, kTile)) * ceil_div(D, kTile) * split;
-    l.total = l.part + (split > 1 ? units * kTile * kTile * sizeof(float) : 0);
+    l.total = l.part + parts_bytes(M, D, dx_most_parts(M, D, F, kAssumedPairs));
     return l;
 }
 
@@ -617,15 +680,24 @@ using namespace rtlynx;
 
 extern "C" {
 
+size_t rtlynx_gated_mlp_block_workspace_size(int64_t M, int64_t D, int64_t D_ff, int mode_down) {
+    if (check_sizes(M, D, D_ff, RTLYNX_ACT_SILU) || mode_down != RTLYNX_MODE_DENSE_SKIP || M <= kFewTokens) return 0;
+    return parts_bytes(M, D, down_parts(M, D, D_ff, kAssumedPairs));
+}
+
 int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, const void* W_down,
                            const void* LA_down, const void* LB_down, void* G, void* U, void* H, void* Y, int64_t M,
-                           int64_t D, int64_t D_ff, int64_t R, int act, int mode_down, void* stream_) {
+                           int64_t D, int64_t D_ff, int64_t R, int act, int mode_down, void* workspace,
+                           size_t ws_bytes, void* stream_) {
     int rc = check_sizes(M, D, D_ff, act);
     if (rc) return rc;
     if (!X || !W_gate || !W_up || !W_down || !H || !Y || (G == nullptr) != (U == nullptr))
         return RTLYNX_ERR_INVALID_ARG;
     rc = validate(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down);
     if (rc) return rc;
+    const size_t need = rtlynx_gated_mlp_block_workspace_size(M, D, D_ff, mode_down);
+    if (need > 0 && (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return RTLYNX_ERR_INVALID_ARG;
     const uint64_t x_bytes = 2ull * M * D, h_bytes = 2ull * M * D_ff, w_bytes = 2ull * D * D_ff;
     const bool lora = mode_down == RTLYNX_MODE_SPARSE && R > 0;
     const Range in[6] = {{X, x_bytes},
@@ -634,13 +706,14 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
                          {W_down, w_bytes},
                          {lora ? LA_down : nullptr, 2ull * D * (lora ? R : 0)},
                          {lora ? LB_down : nullptr, 2ull * D_ff * (lora ? R : 0)}};
-    const Range out[4] = {{H, h_bytes}, {Y, x_bytes}, {G, h_bytes}, {U, h_bytes}};
-    if (!ranges_ok(in, 6, out, 4)) return RTLYNX_ERR_INVALID_ARG;
+    const Range out[5] = {{H, h_bytes}, {Y, x_bytes}, {G, h_bytes}, {U, h_bytes}, {need ? workspace : nullptr, need}};
+    if (!ranges_ok(in, 6, out, 5)) return RTLYNX_ERR_INVALID_ARG;
     int num_sms = 0;
     int* err = nullptr;
     rc = device_info(&num_sms, &err);
     if (rc) return rc;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    const int pairs = num_sms / 2;
     if (M <= kFewTokens) {
         if (launch_gated_few(X, W_gate, W_up, H, G, U, static_cast<int>(M), static_cast<int>(D),
                              static_cast<int>(D_ff), act, stream))
@@ -651,31 +724,66 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
                    ? RTLYNX_ERR_CUDA
                    : RTLYNX_OK;
     }
-
+    {
+        GatedArgs args{};
+        Maps maps{args};
+        args.problems = 1;
+        args.err = err;
+        Problem& p = args.p[0];
+        p.m_pairs = ceil_div(M, kTile);
+        // Tiles of 64 output columns where rounds of them over the pairs end
+        // sooner than rounds of 128: with few tokens, 13824 columns are 108
+        // tiles for 74 pairs (two rounds) or 216 (three of half the length).
+        const int64_t wide = static_cast<int64_t>(p.m_pairs) * ceil_div(D_ff, kHalf);
+        const int64_t thin = static_cast<int64_t>(p.m_pairs) * ceil_div(D_ff, kNarrow / 2);
+        const bool narrow = thin <= 4ll * pairs && ceil_div(thin, pairs) < 2 * ceil_div(wide, pairs);
+        const int columns = narrow ? kNarrow / 2 : kHalf;
+        p.n_tiles = ceil_div(D_ff, columns);
+        p.split = 1;
+        p.k0 = p.k = ceil_div(D, 64);
+        p.a0 = p.a1 = maps.add(X, M, D, false);
+        p.b0 = p.b1 = maps.add(W_gate, D_ff, D, false, columns);
+        maps.add(W_up, D_ff, D, false, columns);
+        p.out[0] = maps.out(H, M, D_ff);
+        p.out[1] = maps.out(G, M, D_ff);
+        p.out[2] = maps.out(U, M, D_ff);
+        if (!maps.ok) return RTLYNX_ERR_CUDA;
+        p.group_n = raster_group(p, pairs);
+        p.rows = static_cast<int>(M);
+        p.cols = static_cast<int>(D_ff);
+        args.units = p.m_pairs * p.n_tiles;
+        int e;
+        if (act == RTLYNX_ACT_SILU)
+            e = narrow ? launch_gated<kGatedForward, RTLYNX_ACT_SILU, kNarrow>(args, num_sms, stream)
+                       : launch_gated<kGatedForward, RTLYNX_ACT_SILU>(args, num_sms, stream);
+        else
+            e = narrow ? launch_gated<kGatedForward, RTLYNX_ACT_GELU, kNarrow>(args, num_sms, stream)
+                       : launch_gated<kGatedForward, RTLYNX_ACT_GELU>(args, num_sms, stream);
+        if (e) return RTLYNX_ERR_CUDA;
+    }
+    if (mode_down == RTLYNX_MODE_SPARSE)
+        return rtlynx_linear(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down, stream_);
     GatedArgs args{};
     Maps maps{args};
     args.problems = 1;
     args.err = err;
     Problem& p = args.p[0];
     p.m_pairs = ceil_div(M, kTile);
-    p.n_tiles = ceil_div(D_ff, kHalf);
-    p.split = 1;
-    p.k0 = p.k = ceil_div(D, 64);
-    p.a0 = p.a1 = maps.add(X, M, D, false);
-    p.b0 = p.b1 = maps.add(W_gate, D_ff, D, false);
-    maps.add(W_up, D_ff, D, false);
+    p.n_tiles = ceil_div(D, kTile);
+    p.split = down_parts(M, D, D_ff, pairs);
+    p.part = static_cast<float*>(workspace);
+    p.k0 = p.k = ceil_div(D_ff, 64);
+    p.a0 = p.a1 = maps.add(H, M, D_ff, false);
+    p.b0 = p.b1 = maps.add(W_down, D, D_ff, false);
+    p.out[0] = maps.out(Y, M, D);
+    p.sum_out = static_cast<uint16_t*>(Y);
     if (!maps.ok) return RTLYNX_ERR_CUDA;
-    p.group_n = raster_group(p, num_sms / 2);
+    p.group_n = raster_group(p, pairs);
     p.rows = static_cast<int>(M);
-    p.cols = static_cast<int>(D_ff);
-    p.out[0] = static_cast<uint16_t*>(H);
-    p.out[1] = static_cast<uint16_t*>(G);
-    p.out[2] = static_cast<uint16_t*>(U);
-    args.units = p.m_pairs * p.n_tiles;
-    const int e = act == RTLYNX_ACT_SILU ? launch_gated<kGatedForward, RTLYNX_ACT_SILU>(args, num_sms, stream)
-                                         : launch_gated<kGatedForward, RTLYNX_ACT_GELU>(args, num_sms, stream);
-    if (e) return RTLYNX_ERR_CUDA;
-    return rtlynx_linear(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down, stream_);
+    p.cols = static_cast<int>(D);
+    args.units = p.m_pairs * p.n_tiles * p.split;
+    if (launch_gated<kStore, 0>(args, num_sms, stream)) return RTLYNX_ERR_CUDA;
+    return p.split > 1 && launch_sum_parts(p, stream) ? RTLYNX_ERR_CUDA : RTLYNX_OK;
 }
 
 size_t rtlynx_gated_mlp_backward_workspace_size(int64_t M, int64_t D, int64_t D_ff) {
@@ -722,12 +830,12 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         p.a0 = p.a1 = maps.add(dY, M, D, false);
         p.b0 = p.b1 = maps.add(W_down, D, D_ff, true);
         p.b_mn = 1;
+        p.out[0] = maps.out(dG, M, D_ff);
+        p.out[1] = maps.out(dU, M, D_ff);
         if (!maps.ok) return RTLYNX_ERR_CUDA;
         p.group_n = raster_group(p, num_sms / 2);
         p.rows = static_cast<int>(M);
         p.cols = static_cast<int>(D_ff);
-        p.out[0] = dG;
-        p.out[1] = dU;
         p.in[0] = static_cast<const uint16_t*>(G);
         p.in[1] = static_cast<const uint16_t*>(U);
         args.units = p.m_pairs * p.n_tiles;
@@ -745,7 +853,8 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         p.n_tiles = ceil_div(cols, kTile);
         p.rows = static_cast<int>(rows);
         p.cols = static_cast<int>(cols);
-        p.out[0] = static_cast<uint16_t*>(out);
+        p.out[0] = maps.out(out, rows, cols);
+        p.sum_out = static_cast<uint16_t*>(out);
         p.group_n = raster_group(p, pairs);
         p.first_unit = args.units;
         args.units += p.m_pairs * p.n_tiles * p.split;
@@ -769,7 +878,7 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         const int64_t tiles = static_cast<int64_t>(m_pairs) * ceil_div(D, kTile);
         const int64_t average = (tiles * (p.k + kUnitCost) + shorts * short_cost) / pairs + 1;
         const int64_t wanted = (p.k + kUnitCost + average - 1) / average;
-        const int most = dx_most_parts(M, D, D_ff, pairs < kAssumedPairs ? pairs : kAssumedPairs);
+        const int most = dx_most_parts(M, D, D_ff, pairs);
         p.split = static_cast<int>(wanted < most ? wanted : most);
         p.part = reinterpret_cast<float*>(base + l.part);
         close(p, M, D, dX);
@@ -796,11 +905,7 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
     if (dW_down) weight_grad(dY, D, H, D_ff, dW_down);
     if (!maps.ok) return RTLYNX_ERR_CUDA;
     if (launch_gated<kStore, 0>(args, num_sms, stream)) return RTLYNX_ERR_CUDA;
-    if (has_dx && args.p[0].split > 1) {
-        const Problem& p = args.p[0];
-        if (launch_dependent(rtlynx_gated_sum_parts_kernel, dim3(p.m_pairs * p.n_tiles * 2, 16), dim3(256), 0, stream, p))
-            return RTLYNX_ERR_CUDA;
-    }
+    if (has_dx && args.p[0].split > 1 && launch_sum_parts(args.p[0], stream)) return RTLYNX_ERR_CUDA;
     return RTLYNX_OK;
 }
 

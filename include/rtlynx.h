@@ -201,22 +201,29 @@ int rtlynx_mlp_block(const void* X, const void* W_up, const void* LA_up, const v
  *   G = X W_gate^T, U = X W_up^T, H = act(G) * U   [M, D_ff], one kernel
  *   Y = layer_down(H)                              [M, D]
  *   act      rtlynx_act: SiLU, x / (1 + exp(-x)), or GELU in its erf form
- *   layer_down runs as rtlynx_linear with mode_down and its LoRA pair
- *   (RTLYNX_MODE_DENSE_SKIP: Y = H W_down^T)
+ *   layer_down: RTLYNX_MODE_DENSE_SKIP, Y = H W_down^T, or RTLYNX_MODE_SPARSE,
+ *   rtlynx_linear with its LoRA pair
  *   X [M, D], W_gate, W_up [D_ff, D], W_down [D, D_ff], LA_down [D, R],
  *   LB_down [R, D_ff], all bf16, device; D and D_ff multiples of 8.
  *   H  caller-owned [M, D_ff] bf16 buffer that receives act(G) * U
  *   G, U  caller-owned [M, D_ff] bf16 buffers that receive the projections, for
  *      rtlynx_gated_mlp_backward; both NULL where no gradient follows
+ *   workspace: rtlynx_gated_mlp_block_workspace_size(M, D, D_ff, mode_down)
+ *      bytes of device memory, 256-byte aligned, for this call until it has
+ *      finished; the size may be 0 (always for invalid sizes, and for a sparse
+ *      down layer, which uses the cached workspace of rtlynx_linear)
  * The projections are accumulated in 32 bits; H is made from them before they
  * are rounded.  Outputs may not share a byte with an input or one another.
  * M > 2^28, D or D_ff > 2^22 give RTLYNX_ERR_UNSUPPORTED.
  */
 typedef enum { RTLYNX_ACT_SILU = 0, RTLYNX_ACT_GELU = 1 } rtlynx_act;
 
+size_t rtlynx_gated_mlp_block_workspace_size(int64_t M, int64_t D, int64_t D_ff, int mode_down);
+
 int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, const void* W_down,
                            const void* LA_down, const void* LB_down, void* G, void* U, void* H, void* Y, int64_t M,
-                           int64_t D, int64_t D_ff, int64_t R, int act, int mode_down, void* stream);
+                           int64_t D, int64_t D_ff, int64_t R, int act, int mode_down, void* workspace,
+                           size_t ws_bytes, void* stream);
 
 /* Gradients of the block with a dense down-projection (mode_down =
  * RTLYNX_MODE_DENSE_SKIP), from dY [M, D] and what the forward call wrote:

@@ -16,10 +16,13 @@ def lib():
     return rl.lib()
 
 
-def forward(lib, sizes=(M, D, F), R=0, act=rl.ACT_SILU, mode=rl.MODE_DENSE_SKIP, la=None, lb=None, **at):
+def forward(lib, sizes=(M, D, F), R=0, act=rl.ACT_SILU, mode=rl.MODE_DENSE_SKIP, la=None, lb=None, ws_bytes=None,
+            **at):
     a = dict(AT, **at)
+    if ws_bytes is None:
+        ws_bytes = lib.rtlynx_gated_mlp_block_workspace_size(*sizes, mode)
     return lib.rtlynx_gated_mlp_block(a["X"], a["W_gate"], a["W_up"], a["W_down"], la, lb, a["G"], a["U"], a["H"],
-                                      a["Y"], *sizes, R, act, mode, None)
+                                      a["Y"], *sizes, R, act, mode, a["ws"], ws_bytes, None)
 
 
 def backward(lib, sizes=(M, D, F), act=rl.ACT_SILU, ws_bytes=None, **at):
@@ -105,6 +108,20 @@ def test_backward_pointers_and_workspace(lib):
     assert backward(lib, ws_bytes=need - 1) == rl.ERR_INVALID_ARG
     assert backward(lib, ws=AT["ws"] + 16) == rl.ERR_INVALID_ARG
     assert backward(lib, ws=AT["H"]) == rl.ERR_INVALID_ARG
+
+
+def test_forward_workspace(lib):
+    """Split down-projections need one: few tiles of a long K."""
+    sizes = (100, 64, 8192)
+    need = lib.rtlynx_gated_mlp_block_workspace_size(*sizes, rl.MODE_DENSE_SKIP)
+    assert need > 0 and need % 256 == 0
+    assert lib.rtlynx_gated_mlp_block_workspace_size(*sizes, rl.MODE_SPARSE) == 0
+    assert lib.rtlynx_gated_mlp_block_workspace_size(100, 60, 8192, rl.MODE_DENSE_SKIP) == 0
+    assert lib.rtlynx_gated_mlp_block_workspace_size(1, 64, 8192, rl.MODE_DENSE_SKIP) == 0
+    assert lib.rtlynx_gated_mlp_block_workspace_size(100000, 5120, 8192, rl.MODE_DENSE_SKIP) == 0
+    for change in (dict(ws=None), dict(ws=AT["ws"] + 16), dict(ws_bytes=need - 1), dict(ws=AT["W_up"]),
+                   dict(ws=AT["Y"]), dict(ws=AT["H"])):
+        assert forward(lib, sizes=sizes, **change) == rl.ERR_INVALID_ARG, change
 
 
 def test_cpu_tensors_are_refused():

@@ -25,7 +25,7 @@ H_STEP = 2.0 ** -8
 
 SIZES = [(1, 8, 8), (1, 64, 136), (2, 1032, 264), (3, 72, 40), (5, 520, 1000), (8, 136, 264), (9, 2056, 552),
          (16, 256, 128), (17, 136, 264), (33, 264, 72), (64, 64, 64), (128, 256, 512), (129, 200, 328), (256, 512, 256),
-         (257, 520, 136), (300, 1032, 520), (700, 264, 1160), (1025, 72, 2056)]
+         (257, 520, 136), (300, 1032, 520), (700, 264, 1160), (1025, 72, 2056), (40, 264, 4104), (520, 136, 6152)]
 
 
 def ints(gen, shape, low, high, density):
@@ -292,7 +292,7 @@ def test_other_stream_and_captured_graph(M):
     assert rl.rtlynx_stream_status() == rl.OK
 
 
-@pytest.mark.parametrize("size", [(5, 72, 136), (150, 136, 264)], ids=str)
+@pytest.mark.parametrize("size", [(5, 72, 136), (150, 136, 264), (70, 136, 4104)], ids=str)
 def test_nothing_else_is_written(size):
     """Guard rows around every output stay as they were."""
     M, D, F = size
@@ -306,7 +306,10 @@ def test_nothing_else_is_written(size):
     W = new(F, D), new(F, D), new(D, F)
     bufs = [guarded(M, F) for _ in range(3)] + [guarded(M, D)]
     G, U, H, Y = (b[1] for b in bufs)
-    rl.rtlynx_gated_mlp_block(X, *W, None, None, G, U, H, Y, M, D, F, 0)
+    n = rl.rtlynx_gated_mlp_block_workspace_size(M, D, F)
+    ws = torch.full((n + 4096,), 7, dtype=torch.uint8, device="cuda")
+    rl.rtlynx_gated_mlp_block(X, *W, None, None, G, U, H, Y, M, D, F, 0, rl.ACT_SILU, rl.MODE_DENSE_SKIP, ws, n)
+    assert (ws[n:] == 7).all()
     grads = [guarded(M, D), guarded(F, D), guarded(F, D), guarded(D, F)]
     n = rl.rtlynx_gated_mlp_backward_workspace_size(M, D, F)
     ws = torch.full((n + 4096,), 7, dtype=torch.uint8, device="cuda")
