@@ -75,53 +75,69 @@ struct GatedArgs {
     CUtensorMap maps[kMaxMaps];
     Problem p[kMaxProblems];
     int problems, units;
-    int longs, extra;  // see unit_at
+    int longs, extra;  // see Units
     int* err;
 };
 
 struct Unit {
-    int problem, mp, nt, kb, ke, part;
+    int problem, mp, nt, kb, ke;
     int index;  // among the problem's units
 };
 
-// Unit i of a CTA pair.  The first `longs` units (dX, whose K is 2 D_ff) are
-// dealt round; the pairs from `rest` on, which have one of them less, take
-// `extra` of the others each instead, and what is left is dealt round.
-__device__ __forceinline__ bool unit_at(int i, int pair, int pairs, const GatedArgs& args, Unit& w) {
-    const int rest = args.longs % pairs;
-    const int own = args.longs / pairs + (pair < rest ? 1 : 0);
-    int u;
-    if (i < own) {
-        u = pair + i * pairs;
-    } else {
-        int j = i - own;
-        if (pair >= rest && j < args.extra) {
-            u = j * (pairs - rest) + pair - rest;
-        } else {
-            if (pair >= rest) j -= args.extra;
-            u = args.extra * (pairs - rest) + j * pairs + pair;
-        }
-        u += args.longs;
-    }
-    if (u >= args.units) return false;
-    int n = 0;
-    while (n + 1 < args.problems && u >= args.p[n + 1].first_unit) ++n;
-    const Problem& p = args.p[n];
-    w.index = u - p.first_unit;
-    const int tile = w.index / p.split;
-    w.problem = n;
-    w.part = w.index - tile * p.split;
-    w.kb = static_cast<int>(static_cast<int64_t>(w.part) * p.k / p.split);
-    w.ke = static_cast<int>(static_cast<int64_t>(w.part + 1) * p.k / p.split);
-    // column tiles in groups of group_n, a group's tiles row pair by row pair
+// Column tiles in groups of group_n, a group's tiles row pair by row pair.
+__device__ __forceinline__ void tile_at(const Problem& p, int tile, int& mp, int& nt) {
     const int per_group = p.m_pairs * p.group_n;
     const int g = tile / per_group;
     const int width = min(p.group_n, p.n_tiles - g * p.group_n);
     const int in_group = tile - g * per_group;
-    w.mp = in_group / width;
-    w.nt = g * p.group_n + in_group % width;
-    return true;
+    mp = in_group / width;
+    nt = g * p.group_n + in_group - mp * width;
 }
+
+// The units of a CTA pair, one after another.  The first `longs` units (dX,
+// whose K is 2 D_ff) are dealt round; the pairs from `rest` on, which have one of
+// them less, take `extra` of the others each instead, and what is left is
+// dealt round.  Divisions are kept out of the way of the common case (nothing
+// split, no long units): every role computes this between two tiles.
+struct Units {
+    int pair, pairs, rest, own, shift;
+
+    __device__ __forceinline__ Units(const GatedArgs& args, int pair_, int pairs_) : pair(pair_), pairs(pairs_) {
+        rest = own = 0;
+        if (args.longs > 0) {
+            rest = args.longs % pairs;
+            own = args.longs / pairs + (pair < rest ? 1 : 0);
+        }
+        shift = args.longs + args.extra * (pairs - rest);  // first unit dealt round after the extra ones
+    }
+
+    __device__ __forceinline__ bool at(int i, const GatedArgs& args, Unit& w) const {
+        int u;
+        if (i < own) {
+            u = pair + i * pairs;
+        } else {
+            const int j = i - own, extra = pair >= rest ? args.extra : 0;
+            u = j < extra ? args.longs + j * (pairs - rest) + pair - rest : shift + (j - extra) * pairs + pair;
+        }
+        if (u >= args.units) return false;
+        int n = 0;
+        while (n + 1 < args.problems && u >= args.p[n + 1].first_unit) ++n;
+        const Problem& p = args.p[n];
+        w.problem = n;
+        w.index = u - p.first_unit;
+        int tile = w.index;
+        w.kb = 0;
+        w.ke = p.k;
+        if (p.split > 1) {
+            tile = w.index / p.split;
+            const int part = w.index - tile * p.split;
+            w.kb = part * p.k / p.split;
+            w.ke = (part + 1) * p.k / p.split;
+        }
+        tile_at(p, tile, w.mp, w.nt);
+        return true;
+    }
+};
 
 __device__ __forceinline__ bool whole_warp_wait(uint64_t* bar, uint32_t parity, int* err) {
     uint32_t ok = 0;
@@ -227,6 +243,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grid_dependency_wait();
     launch_dependents();  // the next kernel's setup may overlap this one
 
+    const Units units(args, pair, num_pairs);
     Unit w;
     if (warp == 0) {
         // The whole warp runs the loop and one elected lane issues, so that
@@ -259,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         };
-        for (int i = 0; ok && unit_at(i, pair, num_pairs, args, w); ++i) {
+        for (int i = 0; ok && units.at(i, args, w); ++i) {
             const Problem& p = args.p[w.problem];
             const int row0 = w.mp * kTile + static_cast<int>(rank) * kHalf;
             const int col0 = EPI == kGatedForward ? w.nt * kColumns : w.nt * kTile + static_cast<int>(rank) * kHalf;
@@ -335,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            for (int local = 0; ok && unit_at(local, pair, num_pairs, args, w); ++local) {
+            for (int local = 0; ok && units.at(local, args, w); ++local) {
                 const Problem& p = args.p[w.problem];
                 const int buf = local & 1;
                 const uint32_t use = static_cast<uint32_t>(local >> 1);
@@ -382,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             turn ^= 1;
         };
-        for (int local = 0; unit_at(local, pair, num_pairs, args, w); ++local) {
+        for (int local = 0; units.at(local, args, w); ++local) {
             const Problem& p = args.p[w.problem];
             const int buf = local & 1;
             const uint32_t use = static_cast<uint32_t>(local >> 1);
@@ -391,6 +408,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t acc = tmem_base + static_cast<uint32_t>(buf * TN) + lane_addr;
             if (!whole_warp_wait(&acc_full[buf], use & 1u, err)) break;
             tc_fence_after();
+            // called once the warp has read its share of the accumulator: the
+            // MMAs of the tile after next may overwrite it
+            bool held = true;
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+                held = false;
+            };
             if constexpr (EPI == kGatedForward) {
                 constexpr int kCols = kColumns / (kEpiWarps / 4);
                 const int c0 = part * kCols;
@@ -402,6 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), g);
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(kColumns + c), v);
                     tmem_ld_wait();
+                    if (c + 32 >= c0 + kCols) release();
                     uint4 packed[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -439,6 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), r);
                     tmem_ld_wait();
+                    if (c + 32 >= c0 + kCols) release();
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         float gf[8], uf[8];
@@ -481,14 +509,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), r);
                     tmem_ld_wait();
+                    if (c + 32 >= (part + 1) * kCols) release();
                     uint4 packed[4];
                     pack32(r, packed);
                     put(p.out[0], packed, col, row0);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+            if (held) release();
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
@@ -518,12 +545,10 @@ __global__ void __launch_bounds__(256) rtlynx_gated_sum_parts_kernel(const __gri
     launch_dependents();
     const int tile = blockIdx.x >> 1, rank = blockIdx.x & 1;
     const int row_in_cta = threadIdx.x & 127, octet = blockIdx.y * 2 + (threadIdx.x >> 7);
-    const int per_group = p.m_pairs * p.group_n;
-    const int g = tile / per_group;
-    const int width = min(p.group_n, p.n_tiles - g * p.group_n);
-    const int in_group = tile - g * per_group;
-    const int row = (in_group / width) * kTile + rank * kHalf + row_in_cta;
-    const int col = (g * p.group_n + in_group % width) * kTile + 8 * octet;
+    int mp, nt;
+    tile_at(p, tile, mp, nt);
+    const int row = mp * kTile + rank * kHalf + row_in_cta;
+    const int col = nt * kTile + 8 * octet;
     if (row >= p.rows || col >= p.cols) return;
     float sum[8] = {};
     for (int s = 0; s < p.split; ++s) {
@@ -646,12 +671,10 @@ size_t parts_bytes(int64_t rows, int64_t cols, int split) {
     return split > 1 ? tiles * split * kTile * kTile * sizeof(float) : 0;
 }
 
-// Y = H Wd^T of the forward call.
-#ifndef DOWN_LEAST
-#define DOWN_LEAST 16
-#endif
+// Y = H Wd^T of the forward call.  Parts of eight stages: at 1024 -> 2816 and
+// 64 tokens the call takes 19.7 us, 22.5 with parts of 16, 20.2 with parts of four.
 int down_parts(int64_t M, int64_t D, int64_t F, int pairs) {
-    return most_parts(M, D, ceil_div(F, 64), pairs < kAssumedPairs ? pairs : kAssumedPairs, DOWN_LEAST);
+    return most_parts(M, D, ceil_div(F, 64), pairs < kAssumedPairs ? pairs : kAssumedPairs, 8);
 }
 
 // dX, K = 2 D_ff
@@ -883,7 +906,7 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         p.part = reinterpret_cast<float*>(base + l.part);
         close(p, M, D, dX);
         args.longs = args.units;
-        // see unit_at: short units that take as long as one dX unit
+        // see Units: short units that take as long as one dX unit
         const int rest = args.longs % pairs;
         if (rest > 0) {
             int64_t extra = (p.k / p.split + kUnitCost) / short_cost;
