@@ -44,12 +44,11 @@ constexpr int kTile = 256;                      // rows of a tile, and accumulat
 constexpr int kHalf = 128;                      // one CTA's share of either operand
 constexpr int kNarrow = 128;                    // accumulator columns of a narrow tile
 constexpr int kOperandBytes = kHalf * 64 * 2;   // 128 x 64 values
-constexpr int kStageBytes = 2 * kOperandBytes;  // A and B
-constexpr int kStages = 6;
+constexpr int kStagingBytes = 6 * 2 * kOperandBytes;  // six stages of A and B; eight where B is half as wide
 constexpr int kEpiWarps = 8;                    // two on each quadrant of tensor-memory lanes, half of the columns each
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kPieceBytes = 32 * 32 * 2;        // 32 rows x 32 columns on their way out
-constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * 2 * kPieceBytes + 1024 + 1024;
+constexpr int kSmemBytes = kStagingBytes + kEpiWarps * 2 * kPieceBytes + 1024 + 1024;
 constexpr int kMaxProblems = 4;
 constexpr int kMaxMaps = 16;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -198,11 +197,12 @@ template <int EPI, int ACT, int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     rtlynx_gated_gemm_kernel(const __grid_constant__ GatedArgs args) {
     constexpr int kColumns = TN / 2;  // rows of B a CTA holds
-    constexpr uint32_t kStageLoads = kOperandBytes + kColumns * 64 * 2;
+    constexpr int kStageBytes = kOperandBytes + kColumns * 64 * 2;
+    constexpr int kStages = kStagingBytes / kStageBytes;
     static_assert(EPI == kGatedForward || TN == kTile, "only the forward epilogue has narrow tiles");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* pieces = smem + kStages * kStageBytes;
+    uint8_t* pieces = smem + kStagingBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(pieces + kEpiWarps * 2 * kPieceBytes);
     uint64_t* empty = full + kStages;
     uint64_t* acc_full = empty + kStages;  // [2]
@@ -266,7 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t dst = smem0 + static_cast<uint32_t>(stage * kStageBytes);
                 const uint32_t bar = full0 + static_cast<uint32_t>(stage) * 8u;
                 if (elect_one()) {
-                    if (leader) mbar_arrive_expect_tx(&full[stage], 2u * kStageLoads);
+                    if (leader) mbar_arrive_expect_tx(&full[stage], 2u * kStageBytes);
                     load_operand<A_MN>(dst, ma, bar, k, row0);
                     load_operand<B_MN>(dst + kOperandBytes, mb, bar, k, col0);
                 }
@@ -492,6 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 constexpr int kCols = kTile / (kEpiWarps / 4);
 #pragma unroll 1
                 for (int c = part * kCols; c < (part + 1) * kCols; c += 32) {
+                    if (row0 >= p.rows || w.nt * kTile + c >= p.cols) break;  // never read; the same in the whole warp
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), r);
                     tmem_ld_wait();

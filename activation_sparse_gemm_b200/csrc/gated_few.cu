@@ -30,8 +30,6 @@
 namespace rtlynx {
 namespace {
 
-constexpr int kFewWarps = 8;
-constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewRows = 16;  // output channels of a block
 
 struct FewArgs {
@@ -59,9 +57,10 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 }
 
 // GATED: two matrices, act(first) * second; otherwise the one product.
-// TILES: tokens in eights.
-template <bool GATED, int TILES, int ACT>
-__global__ void __launch_bounds__(kFewThreads) rtlynx_gated_few_kernel(const FewArgs args) {
+// TILES: tokens in eights.  WARPS: warps of a block.
+template <bool GATED, int TILES, int ACT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) rtlynx_gated_few_kernel(const FewArgs args) {
+    constexpr int kFewWarps = WARPS, kFewThreads = 32 * WARPS;
     constexpr int kMats = GATED ? 2 : 1;
     constexpr int kUnroll = GATED ? 2 : 4;
     constexpr int kSums = kMats * TILES * 4;
@@ -169,11 +168,24 @@ __global__ void __launch_bounds__(kFewThreads) rtlynx_gated_few_kernel(const Few
     }
 }
 
+template <bool GATED, int ACT, int WARPS>
+int launch_warps(const FewArgs& args, cudaStream_t stream) {
+    const dim3 grid((args.N + kFewRows - 1) / kFewRows), block(32 * WARPS);
+    if (args.M <= 8) return launch_dependent(rtlynx_gated_few_kernel<GATED, 1, ACT, WARPS>, grid, block, 0, stream, args);
+    return launch_dependent(rtlynx_gated_few_kernel<GATED, 2, ACT, WARPS>, grid, block, 0, stream, args);
+}
+
 template <bool GATED, int ACT>
 int launch_few(const FewArgs& args, cudaStream_t stream) {
-    const dim3 grid((args.N + kFewRows - 1) / kFewRows), block(kFewThreads);
-    if (args.M <= 8) return launch_dependent(rtlynx_gated_few_kernel<GATED, 1, ACT>, grid, block, 0, stream, args);
-    return launch_dependent(rtlynx_gated_few_kernel<GATED, 2, ACT>, grid, block, 0, stream, args);
+    // Sixteen warps where there are no more blocks than SMs, so that enough
+    // loads are in flight: at 2056 -> 5512 and 11 tokens the call takes 19.3 us,
+    // 25.1 with eight.  With more blocks eight are as good or better (70 against
+    // 77 us at 5120 -> 13824, one token).
+    int num_sms = 0;
+    int* err = nullptr;
+    if (device_info(&num_sms, &err)) return static_cast<int>(cudaErrorInvalidDevice);
+    const int blocks = (args.N + kFewRows - 1) / kFewRows;
+    return blocks <= num_sms ? launch_warps<GATED, ACT, 16>(args, stream) : launch_warps<GATED, ACT, 8>(args, stream);
 }
 
 }  // namespace
