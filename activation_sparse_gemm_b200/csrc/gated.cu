@@ -502,18 +502,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
                 }
             } else {
+                // all of the warp's share at once, so that the accumulator is
+                // free before the first piece goes out
                 constexpr int kCols = kTile / (kEpiWarps / 4);
-#pragma unroll 1
-                for (int c = part * kCols; c < (part + 1) * kCols; c += 32) {
-                    const int col = w.nt * kTile + c;
-                    if (row0 >= p.rows || col >= p.cols) break;  // the same in the whole warp
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), r);
-                    tmem_ld_wait();
-                    if (c + 32 >= (part + 1) * kCols) release();
-                    uint4 packed[4];
-                    pack32(r, packed);
-                    put(p.out[0], packed, col, row0);
+                const int c0 = part * kCols;
+                uint32_t r[kCols / 32][32];
+#pragma unroll
+                for (int i = 0; i < kCols / 32; ++i) tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c0 + 32 * i), r[i]);
+                tmem_ld_wait();
+                release();
+#pragma unroll
+                for (int i = 0; i < kCols / 32; ++i) {
+                    const int col = w.nt * kTile + c0 + 32 * i;
+                    if (row0 < p.rows && col < p.cols) {  // the same in the whole warp
+                        uint4 packed[4];
+                        pack32(r[i], packed);
+                        put(p.out[0], packed, col, row0);
+                    }
                 }
             }
             if (held) release();
@@ -655,7 +660,7 @@ constexpr int kAssumedPairs = 74;  // sizes the workspace; a GPU with fewer pair
 
 // Stages' worth of time that a unit costs beside its stages (filling the
 // pipeline, its share of the epilogue).
-constexpr int kUnitCost = 8;
+constexpr int kUnitCost = 4;
 
 // Most parts that the tiles of a [rows, cols] product are cut into along its
 // `stages` of K: where tiles are fewer than CTA pairs each pair gets at most
