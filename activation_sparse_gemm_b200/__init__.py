@@ -130,13 +130,13 @@ def lib() -> ctypes.CDLL:
         L.rtlynx_kernel_launches.restype = i
         L.rtlynx_schedule_info.argtypes = [i64, i64, i64, i64, i, ctypes.POINTER(Schedule)]
         L.rtlynx_schedule_info.restype = i
-        L.rtlynx_gated_mlp_block.argtypes = [p] * 10 + [i64, i64, i64, i64, i, i, p, ctypes.c_size_t, p]
+        L.rtlynx_gated_mlp_block.argtypes = [p] * 11 + [i64, i64, i64, i64, i, i, p, ctypes.c_size_t, p]
         L.rtlynx_gated_mlp_block.restype = i
         L.rtlynx_gated_mlp_block_workspace_size.argtypes = [i64, i64, i64, i]
         L.rtlynx_gated_mlp_block_workspace_size.restype = ctypes.c_size_t
         L.rtlynx_gated_mlp_backward_workspace_size.argtypes = [i64, i64, i64]
         L.rtlynx_gated_mlp_backward_workspace_size.restype = ctypes.c_size_t
-        L.rtlynx_gated_mlp_backward.argtypes = [p] * 12 + [i64, i64, i64, i, p, ctypes.c_size_t, p]
+        L.rtlynx_gated_mlp_backward.argtypes = [p] * 13 + [i64, i64, i64, i, p, ctypes.c_size_t, p]
         L.rtlynx_gated_mlp_backward.restype = i
         hv, spec, f = ctypes.POINTER(HeadsView), ctypes.POINTER(RopeSpec), ctypes.c_float
         L.rtlynx_rope.argtypes = [hv, hv, hv, hv, i64, i64, i64, i, spec, p, i64, i64, i64, p]
@@ -281,12 +281,12 @@ def rtlynx_gated_mlp_block_workspace_size(M, D, D_ff, mode_down=MODE_DENSE_SKIP)
     return int(lib().rtlynx_gated_mlp_block_workspace_size(M, D, D_ff, mode_down))
 
 
-def rtlynx_gated_mlp_block(X, W_gate, W_up, W_down, LA_down, LB_down, G, U, H, Y, M, D, D_ff, R, act, mode_down,
+def rtlynx_gated_mlp_block(X, W_gate, W_up, W_down, LA_down, LB_down, G, U, low, H, Y, M, D, D_ff, R, act, mode_down,
                            workspace, ws_bytes, stream=None) -> int:
     """H = act(X W_gate^T) * (X W_up^T) [M, D_ff], Y = layer_down(H) [M, D]; see include/rtlynx.h."""
     return _check(lib().rtlynx_gated_mlp_block(_ptr(X), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _ptr(LA_down),
-                                               _ptr(LB_down), _ptr(G), _ptr(U), _ptr(H), _ptr(Y), M, D, D_ff, R, act,
-                                               mode_down, _ptr(workspace), ws_bytes, _stream(stream)),
+                                               _ptr(LB_down), _ptr(G), _ptr(U), _ptr(low), _ptr(H), _ptr(Y), M, D, D_ff,
+                                               R, act, mode_down, _ptr(workspace), ws_bytes, _stream(stream)),
                   "rtlynx_gated_mlp_block")
 
 
@@ -294,10 +294,10 @@ def rtlynx_gated_mlp_backward_workspace_size(M, D, D_ff) -> int:
     return int(lib().rtlynx_gated_mlp_backward_workspace_size(M, D, D_ff))
 
 
-def rtlynx_gated_mlp_backward(dY, X, W_gate, W_up, W_down, G, U, H, dX, dW_gate, dW_up, dW_down, M, D, D_ff, act,
+def rtlynx_gated_mlp_backward(dY, X, W_gate, W_up, W_down, G, U, low, H, dX, dW_gate, dW_up, dW_down, M, D, D_ff, act,
                               workspace, ws_bytes, stream=None) -> int:
     return _check(lib().rtlynx_gated_mlp_backward(_ptr(dY), _ptr(X), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _ptr(G),
-                                                  _ptr(U), _ptr(H), _ptr(dX), _ptr(dW_gate), _ptr(dW_up),
+                                                  _ptr(U), _ptr(low), _ptr(H), _ptr(dX), _ptr(dW_gate), _ptr(dW_up),
                                                   _ptr(dW_down), M, D, D_ff, act, _ptr(workspace), ws_bytes,
                                                   _stream(stream)), "rtlynx_gated_mlp_backward")
 
@@ -579,11 +579,12 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, w_q, w_k, positions, rope, eps=1
     return dq, dk, dw_q, dw_k
 
 
-def _matrix(t, rows, cols, device, what):
+def _matrix(t, rows, cols, device, what, dtype=None):
     """The address of t, checked: a contiguous bf16 CUDA matrix of this shape on this device."""
     import torch
-    if t.dtype != torch.bfloat16 or t.device != device or t.shape != (rows, cols) or not t.is_contiguous():
-        raise ValueError(f"{what}: contiguous bf16 {(rows, cols)} on {device}, got {t.dtype} {tuple(t.shape)} on "
+    dtype = dtype or torch.bfloat16
+    if t.dtype != dtype or t.device != device or t.shape != (rows, cols) or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous {dtype} {(rows, cols)} on {device}, got {t.dtype} {tuple(t.shape)} on "
                          f"{t.device}")
     return t.data_ptr()
 
@@ -602,7 +603,8 @@ def gated_mlp(X, W_gate, W_up, W_down, act=ACT_SILU, L_A=None, L_B=None, mode_do
     W_down [D, D_ff].
 
     With mode_down=MODE_SPARSE the down-projection is the activation-sparse layer with the LoRA pair L_A [D, R],
-    L_B [R, D_ff].  With save=True the result is (Y, saved), saved = (G, U, H) for gated_mlp_backward."""
+    L_B [R, D_ff].  With save=True the result is (Y, saved), saved = (G, U, low, H) for gated_mlp_backward
+    (low: the bits of G and U below bf16's, as int16; see include/rtlynx.h)."""
     import torch
     (M, D, F), at = _gated_inputs(X, W_gate, W_up, W_down)
     device = X.device
@@ -617,13 +619,15 @@ def gated_mlp(X, W_gate, W_up, W_down, act=ACT_SILU, L_A=None, L_B=None, mode_do
         else:
             Y, y = out, _matrix(out, M, D, device, "out")
         H = torch.empty((M, F), dtype=X.dtype, device=device)
-        G, U = (torch.empty_like(H), torch.empty_like(H)) if save else (None, None)
+        G = U = low = None
+        if save:
+            G, U, low = torch.empty_like(H), torch.empty_like(H), torch.empty_like(H, dtype=torch.int16)
         ws_bytes = lib().rtlynx_gated_mlp_block_workspace_size(M, D, F, mode_down)
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
-        status = lib().rtlynx_gated_mlp_block(*at, la, lb, _ptr(G), _ptr(U), H.data_ptr(), y, M, D, F, R, act,
-                                              mode_down, _ptr(ws), ws_bytes, handle)
+        status = lib().rtlynx_gated_mlp_block(*at, la, lb, _ptr(G), _ptr(U), _ptr(low), H.data_ptr(), y, M, D, F,
+                                              R, act, mode_down, _ptr(ws), ws_bytes, handle)
     _check(status, "rtlynx_gated_mlp_block")
-    return (Y, (G, U, H)) if save else Y
+    return (Y, (G, U, low, H)) if save else Y
 
 
 def gated_mlp_backward(dY, X, W_gate, W_up, W_down, saved, act=ACT_SILU, needs=(True, True, True, True), stream=None):
@@ -634,7 +638,8 @@ def gated_mlp_backward(dY, X, W_gate, W_up, W_down, saved, act=ACT_SILU, needs=(
     (M, D, F), at = _gated_inputs(X, W_gate, W_up, W_down)
     device = X.device
     dy = _matrix(dY, M, D, device, "dY")
-    kept = [_matrix(t, M, F, device, name) for t, name in zip(saved, "GUH")]
+    kept = [_matrix(t, M, F, device, name, torch.int16 if name == "low" else None)
+            for t, name in zip(saved, ("G", "U", "low", "H"), strict=True)]
     handle, ctx = _launch_on(device, stream)
     with ctx:
         grads = tuple(torch.empty_like(t) if need else None for t, need in zip((X, W_gate, W_up, W_down), needs))

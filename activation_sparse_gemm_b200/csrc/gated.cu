@@ -26,9 +26,12 @@
 // 64 contiguous elements by 64 rows either way, and the MMA's descriptors say
 // which of the two is K.
 //
-// fp32 accumulation throughout.  G, U, H, dG and dU are rounded to bf16 once:
-// they are the operands of the next MMA (which takes bf16), and what backward
-// keeps.  H is made from the unrounded G and U.
+// fp32 accumulation throughout.  H, dG and dU are rounded to bf16 once, as the
+// next MMA takes bf16; H is made from the unrounded G and U.  G and U are no
+// operand of anything, so what backward keeps of them is 24 bits: the upper 16
+// of each, and the next eight of both in one more 16-bit array.  Kept as bf16
+// they would add two roundings to dG and dU (error of the weights' gradients
+// 1.85 times a bf16 rounding, 1.4 so).
 #include "../../include/rtlynx.h"
 #include "act.cuh"
 #include "internal.h"
@@ -64,9 +67,9 @@ struct Problem {
     int a0, b0, a1, b1;
     int a_mn, b_mn;             // operand is MN-major
     int rows, cols;             // of the output
-    int out[3];                 // maps of the outputs; forward: H, G, U (G, U may be -1); backward: dG, dU
+    int out[4];                 // maps of the outputs; forward: H, G, U, low (the last three may be -1); backward: dG, dU
     uint16_t* sum_out;          // split > 1: the output of the summing kernel
-    const uint16_t* in[2];      // backward: G, U
+    const uint16_t* in[3];      // backward: G, U, low
     float* part;                // split > 1: fp32 partial tiles
 };
 
@@ -183,12 +186,37 @@ __device__ __forceinline__ void pack32(const uint32_t (&r)[32], uint4 (&v)[4]) {
     }
 }
 
-__device__ __forceinline__ void unpack8(uint4 u, float* v) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// The upper 16 bits of 32 values.
+__device__ __forceinline__ void high32(const uint32_t (&r)[32], uint4 (&v)[4]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        v[q] = make_uint4(__byte_perm(r[8 * q], r[8 * q + 1], 0x7632), __byte_perm(r[8 * q + 2], r[8 * q + 3], 0x7632),
+                          __byte_perm(r[8 * q + 4], r[8 * q + 5], 0x7632), __byte_perm(r[8 * q + 6], r[8 * q + 7], 0x7632));
+}
+
+// The eight bits below those, of two arrays: the first's in the low byte.
+__device__ __forceinline__ uint32_t low2(uint32_t a0, uint32_t b0, uint32_t a1, uint32_t b1) {
+    return __byte_perm(__byte_perm(a0, b0, 0x0051), __byte_perm(a1, b1, 0x0051), 0x5410);
+}
+__device__ __forceinline__ void low32(const uint32_t (&a)[32], const uint32_t (&b)[32], uint4 (&v)[4]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int j = 8 * q;
+        v[q] = make_uint4(low2(a[j], b[j], a[j + 1], b[j + 1]), low2(a[j + 2], b[j + 2], a[j + 3], b[j + 3]),
+                          low2(a[j + 4], b[j + 4], a[j + 5], b[j + 5]), low2(a[j + 6], b[j + 6], a[j + 7], b[j + 7]));
+    }
+}
+
+// Eight values of G and U from their upper bits and the shared lower ones (the
+// last byte repeated below itself, so that what was cut off is not biased).
+__device__ __forceinline__ void restore8(uint4 g, uint4 u, uint4 low, float* gf, float* uf) {
+    const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w}, lw[4] = {low.x, low.y, low.z, low.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        gf[2 * i] = __uint_as_float(__byte_perm(gw[i], lw[i], 0x1044));
+        uf[2 * i] = __uint_as_float(__byte_perm(uw[i], lw[i], 0x1055));
+        gf[2 * i + 1] = __uint_as_float(__byte_perm(gw[i], lw[i], 0x3266));
+        uf[2 * i + 1] = __uint_as_float(__byte_perm(uw[i], lw[i], 0x3277));
     }
 }
 
@@ -440,10 +468,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     put(p.out[0], packed, col, row0);
                     if (p.out[1] >= 0) {
-                        pack32(g, packed);
+                        high32(g, packed);
                         put(p.out[1], packed, col, row0);
-                        pack32(v, packed);
+                        high32(v, packed);
                         put(p.out[2], packed, col, row0);
+                        low32(g, v, packed);
+                        put(p.out[3], packed, col, row0);
                     }
                 }
             } else if constexpr (EPI == kGatedBackward) {
@@ -452,16 +482,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = c0; c < c0 + kCols; c += 32) {
                     uint32_t r[32];
-                    uint4 gp[4], up[4];
+                    uint4 gp[4], up[4], lp[4];
                     const int col0 = w.nt * kTile + c, row = row0 + lane;
                     if (row0 >= p.rows || col0 >= p.cols) break;  // the same in the whole warp
                     const size_t at = static_cast<size_t>(row) * p.cols + col0;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        gp[q] = up[q] = make_uint4(0, 0, 0, 0);
+                        gp[q] = up[q] = lp[q] = make_uint4(0, 0, 0, 0);
                         if (row < p.rows && col0 + 8 * q < p.cols) {
                             gp[q] = __ldg(reinterpret_cast<const uint4*>(p.in[0] + at + 8 * q));
                             up[q] = __ldg(reinterpret_cast<const uint4*>(p.in[1] + at + 8 * q));
+                            lp[q] = __ldg(reinterpret_cast<const uint4*>(p.in[2] + at + 8 * q));
                         }
                     }
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), r);
@@ -470,8 +501,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         float gf[8], uf[8];
-                        unpack8(gp[q], gf);
-                        unpack8(up[q], uf);
+                        restore8(gp[q], up[q], lp[q], gf, uf);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float dh = __uint_as_float(r[8 * q + j]);
@@ -715,12 +745,13 @@ size_t rtlynx_gated_mlp_block_workspace_size(int64_t M, int64_t D, int64_t D_ff,
 }
 
 int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, const void* W_down,
-                           const void* LA_down, const void* LB_down, void* G, void* U, void* H, void* Y, int64_t M,
+                           const void* LA_down, const void* LB_down, void* G, void* U, void* low, void* H, void* Y, int64_t M,
                            int64_t D, int64_t D_ff, int64_t R, int act, int mode_down, void* workspace,
                            size_t ws_bytes, void* stream_) {
     int rc = check_sizes(M, D, D_ff, act);
     if (rc) return rc;
-    if (!X || !W_gate || !W_up || !W_down || !H || !Y || (G == nullptr) != (U == nullptr))
+    if (!X || !W_gate || !W_up || !W_down || !H || !Y || (G == nullptr) != (U == nullptr) ||
+        (G == nullptr) != (low == nullptr))
         return RTLYNX_ERR_INVALID_ARG;
     rc = validate(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down);
     if (rc) return rc;
@@ -735,8 +766,9 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
                          {W_down, w_bytes},
                          {lora ? LA_down : nullptr, 2ull * D * (lora ? R : 0)},
                          {lora ? LB_down : nullptr, 2ull * D_ff * (lora ? R : 0)}};
-    const Range out[5] = {{H, h_bytes}, {Y, x_bytes}, {G, h_bytes}, {U, h_bytes}, {need ? workspace : nullptr, need}};
-    if (!ranges_ok(in, 6, out, 5)) return RTLYNX_ERR_INVALID_ARG;
+    const Range out[6] = {{H, h_bytes}, {Y, x_bytes}, {G, h_bytes}, {U, h_bytes}, {low, h_bytes},
+                          {need ? workspace : nullptr, need}};
+    if (!ranges_ok(in, 6, out, 6)) return RTLYNX_ERR_INVALID_ARG;
     int num_sms = 0;
     int* err = nullptr;
     rc = device_info(&num_sms, &err);
@@ -744,7 +776,7 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     const int pairs = num_sms / 2;
     if (M <= kFewTokens) {
-        if (launch_gated_few(X, W_gate, W_up, H, G, U, static_cast<int>(M), static_cast<int>(D),
+        if (launch_gated_few(X, W_gate, W_up, H, G, U, low, static_cast<int>(M), static_cast<int>(D),
                              static_cast<int>(D_ff), act, stream))
             return RTLYNX_ERR_CUDA;
         if (mode_down == RTLYNX_MODE_SPARSE)
@@ -776,6 +808,7 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
         p.out[0] = maps.out(H, M, D_ff);
         p.out[1] = maps.out(G, M, D_ff);
         p.out[2] = maps.out(U, M, D_ff);
+        p.out[3] = maps.out(low, M, D_ff);
         if (!maps.ok) return RTLYNX_ERR_CUDA;
         p.group_n = raster_group(p, pairs);
         p.rows = static_cast<int>(M);
@@ -821,19 +854,20 @@ size_t rtlynx_gated_mlp_backward_workspace_size(int64_t M, int64_t D, int64_t D_
 }
 
 int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate, const void* W_up, const void* W_down,
-                              const void* G, const void* U, const void* H, void* dX, void* dW_gate, void* dW_up,
+                              const void* G, const void* U, const void* low, const void* H, void* dX, void* dW_gate, void* dW_up,
                               void* dW_down, int64_t M, int64_t D, int64_t D_ff, int act, void* workspace,
                               size_t ws_bytes, void* stream_) {
     int rc = check_sizes(M, D, D_ff, act);
     if (rc) return rc;
-    if (!dY || !X || !W_gate || !W_up || !W_down || !G || !U || !H || !workspace) return RTLYNX_ERR_INVALID_ARG;
+    if (!dY || !X || !W_gate || !W_up || !W_down || !G || !U || !low || !H || !workspace)
+         return RTLYNX_ERR_INVALID_ARG;
     const BackwardLayout l = backward_layout(M, D, D_ff);
     if (ws_bytes < l.total || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return RTLYNX_ERR_INVALID_ARG;
     const uint64_t x_bytes = 2ull * M * D, h_bytes = 2ull * M * D_ff, w_bytes = 2ull * D * D_ff;
-    const Range in[8] = {{dY, x_bytes},     {X, x_bytes}, {W_gate, w_bytes}, {W_up, w_bytes},
-                         {W_down, w_bytes}, {G, h_bytes}, {U, h_bytes},      {H, h_bytes}};
+    const Range in[9] = {{dY, x_bytes}, {X, x_bytes}, {W_gate, w_bytes}, {W_up, w_bytes}, {W_down, w_bytes},
+                         {G, h_bytes},  {U, h_bytes}, {low, h_bytes},    {H, h_bytes}};
     const Range out[5] = {{dX, x_bytes}, {dW_gate, w_bytes}, {dW_up, w_bytes}, {dW_down, w_bytes}, {workspace, l.total}};
-    if (!ranges_ok(in, 8, out, 5)) return RTLYNX_ERR_INVALID_ARG;
+    if (!ranges_ok(in, 9, out, 5)) return RTLYNX_ERR_INVALID_ARG;
     if (!dX && !dW_gate && !dW_up && !dW_down) return RTLYNX_OK;
     int num_sms = 0;
     int* err = nullptr;
@@ -867,6 +901,7 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         p.cols = static_cast<int>(D_ff);
         p.in[0] = static_cast<const uint16_t*>(G);
         p.in[1] = static_cast<const uint16_t*>(U);
+        p.in[2] = static_cast<const uint16_t*>(low);
         args.units = p.m_pairs * p.n_tiles;
         const int e = act == RTLYNX_ACT_SILU ? launch_gated<kGatedBackward, RTLYNX_ACT_SILU>(args, num_sms, stream)
                                              : launch_gated<kGatedBackward, RTLYNX_ACT_GELU>(args, num_sms, stream);

@@ -35,7 +35,7 @@ constexpr int kFewRows = 16;  // output channels of a block
 struct FewArgs {
     const uint16_t* x;      // [M, K]
     const uint16_t* w[2];   // [N, K]: gate and up, or the one matrix
-    uint16_t* out[3];       // [M, N]: H, G, U (G, U may be null), or the one output
+    uint16_t* out[4];       // [M, N]: H, G, U, low (the last three may be null, see gated.cu), or the one output
     int M, N, K;
 };
 
@@ -159,8 +159,10 @@ __global__ void __launch_bounds__(32 * WARPS) rtlynx_gated_few_kernel(const FewA
         if constexpr (GATED) {
             args.out[0][at] = __bfloat16_as_ushort(__float2bfloat16_rn(act_value<ACT>(total[0]) * total[1]));
             if (args.out[1]) {
-                args.out[1][at] = __bfloat16_as_ushort(__float2bfloat16_rn(total[0]));
-                args.out[2][at] = __bfloat16_as_ushort(__float2bfloat16_rn(total[1]));
+                const uint32_t gate = __float_as_uint(total[0]), up = __float_as_uint(total[1]);
+                args.out[1][at] = static_cast<uint16_t>(gate >> 16);
+                args.out[2][at] = static_cast<uint16_t>(up >> 16);
+                args.out[3][at] = static_cast<uint16_t>((gate >> 8 & 0xFFu) | (up & 0xFF00u));
             }
         } else {
             args.out[0][at] = __bfloat16_as_ushort(__float2bfloat16_rn(total[0]));
@@ -190,8 +192,8 @@ int launch_few(const FewArgs& args, cudaStream_t stream) {
 
 }  // namespace
 
-int launch_gated_few(const void* X, const void* W_gate, const void* W_up, void* H, void* G, void* U, int M, int D,
-                     int D_ff, int act, cudaStream_t stream) {
+int launch_gated_few(const void* X, const void* W_gate, const void* W_up, void* H, void* G, void* U, void* low, int M,
+                     int D, int D_ff, int act, cudaStream_t stream) {
     FewArgs args{};
     args.x = static_cast<const uint16_t*>(X);
     args.w[0] = static_cast<const uint16_t*>(W_gate);
@@ -199,6 +201,7 @@ int launch_gated_few(const void* X, const void* W_gate, const void* W_up, void* 
     args.out[0] = static_cast<uint16_t*>(H);
     args.out[1] = static_cast<uint16_t*>(G);
     args.out[2] = static_cast<uint16_t*>(U);
+    args.out[3] = static_cast<uint16_t*>(low);
     args.M = M, args.N = D_ff, args.K = D;
     return act == RTLYNX_ACT_SILU ? launch_few<true, RTLYNX_ACT_SILU>(args, stream)
                                   : launch_few<true, RTLYNX_ACT_GELU>(args, stream);

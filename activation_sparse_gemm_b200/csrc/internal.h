@@ -169,10 +169,10 @@ int launch_small(const Dims& d, const void* X, const void* W, const void* L_A, c
                  const Workspace& ws, void* Y, int* err, cudaStream_t stream);
 
 // The gated feed-forward block for at most kFewTokens tokens (gated_few.cu):
-// H (and G, U unless null) from X; Y = H W_down^T.
+// H (and G, U, low unless null) from X; Y = H W_down^T.
 constexpr int kFewTokens = 16;
-int launch_gated_few(const void* X, const void* W_gate, const void* W_up, void* H, void* G, void* U, int M, int D,
-                     int D_ff, int act, cudaStream_t stream);
+int launch_gated_few(const void* X, const void* W_gate, const void* W_up, void* H, void* G, void* U, void* low, int M,
+                     int D, int D_ff, int act, cudaStream_t stream);
 int launch_down_few(const void* H, const void* W_down, void* Y, int M, int D_ff, int D, cudaStream_t stream);
 
 int launch_wait_selftest(int* err, uint64_t limit_ns, cudaStream_t stream);

@@ -206,8 +206,11 @@ int rtlynx_mlp_block(const void* X, const void* W_up, const void* LA_up, const v
  *   X [M, D], W_gate, W_up [D_ff, D], W_down [D, D_ff], LA_down [D, R],
  *   LB_down [R, D_ff], all bf16, device; D and D_ff multiples of 8.
  *   H  caller-owned [M, D_ff] bf16 buffer that receives act(G) * U
- *   G, U  caller-owned [M, D_ff] bf16 buffers that receive the projections, for
- *      rtlynx_gated_mlp_backward; both NULL where no gradient follows
+ *   G, U, low  caller-owned [M, D_ff] buffers of 16-bit values that receive the
+ *      projections for rtlynx_gated_mlp_backward, 24 bits of each: G and U their
+ *      upper 16 (read as bf16: the projections, cut off), low the next eight of
+ *      G in its low byte and of U in its high one; all three NULL where no
+ *      gradient follows
  *   workspace: rtlynx_gated_mlp_block_workspace_size(M, D, D_ff, mode_down)
  *      bytes of device memory, 256-byte aligned, for this call until it has
  *      finished; the size may be 0 (always for invalid sizes, and for a sparse
@@ -221,7 +224,7 @@ typedef enum { RTLYNX_ACT_SILU = 0, RTLYNX_ACT_GELU = 1 } rtlynx_act;
 size_t rtlynx_gated_mlp_block_workspace_size(int64_t M, int64_t D, int64_t D_ff, int mode_down);
 
 int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, const void* W_down,
-                           const void* LA_down, const void* LB_down, void* G, void* U, void* H, void* Y, int64_t M,
+                           const void* LA_down, const void* LB_down, void* G, void* U, void* low, void* H, void* Y, int64_t M,
                            int64_t D, int64_t D_ff, int64_t R, int act, int mode_down, void* workspace,
                            size_t ws_bytes, void* stream);
 
@@ -238,8 +241,8 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
 size_t rtlynx_gated_mlp_backward_workspace_size(int64_t M, int64_t D, int64_t D_ff);
 
 int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate, const void* W_up, const void* W_down,
-                              const void* G, const void* U, const void* H, void* dX, void* dW_gate, void* dW_up,
-                              void* dW_down, int64_t M, int64_t D, int64_t D_ff, int act, void* workspace,
+                              const void* G, const void* U, const void* low, const void* H, void* dX,
+                              void* dW_gate, void* dW_up, void* dW_down, int64_t M, int64_t D, int64_t D_ff, int act, void* workspace,
                               size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- query and key heads

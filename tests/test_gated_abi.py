@@ -6,7 +6,7 @@ import activation_sparse_gemm_b200 as rl
 from activation_sparse_gemm_b200 import build as rl_build
 
 M, D, F = 6, 64, 128
-NAMES = ("X", "W_gate", "W_up", "W_down", "G", "U", "H", "Y", "dY", "dX", "dW_gate", "dW_up", "dW_down", "ws")
+NAMES = ("X", "W_gate", "W_up", "W_down", "G", "U", "low", "H", "Y", "dY", "dX", "dW_gate", "dW_up", "dW_down", "ws")
 AT = {n: (i + 1) << 24 for i, n in enumerate(NAMES)}
 
 
@@ -21,16 +21,16 @@ def forward(lib, sizes=(M, D, F), R=0, act=rl.ACT_SILU, mode=rl.MODE_DENSE_SKIP,
     a = dict(AT, **at)
     if ws_bytes is None:
         ws_bytes = lib.rtlynx_gated_mlp_block_workspace_size(*sizes, mode)
-    return lib.rtlynx_gated_mlp_block(a["X"], a["W_gate"], a["W_up"], a["W_down"], la, lb, a["G"], a["U"], a["H"],
-                                      a["Y"], *sizes, R, act, mode, a["ws"], ws_bytes, None)
+    return lib.rtlynx_gated_mlp_block(a["X"], a["W_gate"], a["W_up"], a["W_down"], la, lb, a["G"], a["U"], a["low"],
+                                      a["H"], a["Y"], *sizes, R, act, mode, a["ws"], ws_bytes, None)
 
 
 def backward(lib, sizes=(M, D, F), act=rl.ACT_SILU, ws_bytes=None, **at):
     a = dict(AT, **at)
     if ws_bytes is None:
         ws_bytes = max(lib.rtlynx_gated_mlp_backward_workspace_size(M, D, F), 1)
-    return lib.rtlynx_gated_mlp_backward(a["dY"], a["X"], a["W_gate"], a["W_up"], a["W_down"], a["G"], a["U"], a["H"],
-                                         a["dX"], a["dW_gate"], a["dW_up"], a["dW_down"], *sizes, act, a["ws"],
+    return lib.rtlynx_gated_mlp_backward(a["dY"], a["X"], a["W_gate"], a["W_up"], a["W_down"], a["G"], a["U"], a["low"],
+                                         a["H"], a["dX"], a["dW_gate"], a["dW_up"], a["dW_down"], *sizes, act, a["ws"],
                                          ws_bytes, None)
 
 
@@ -39,7 +39,7 @@ def test_valid_calls_pass_the_checks(lib):
     if torch.cuda.is_available():
         pytest.skip("would launch")
     assert forward(lib) != rl.ERR_INVALID_ARG
-    assert forward(lib, G=None, U=None) != rl.ERR_INVALID_ARG
+    assert forward(lib, G=None, U=None, low=None) != rl.ERR_INVALID_ARG
     assert backward(lib) != rl.ERR_INVALID_ARG
     assert backward(lib, dX=None, dW_gate=None, dW_up=None, dW_down=None) == rl.OK
 
@@ -66,9 +66,11 @@ def test_forward_pointers(lib, name):
     assert forward(lib, **{name: AT[name] + 8}) == rl.ERR_INVALID_ARG
 
 
-def test_forward_saves_both_projections_or_none(lib):
+def test_forward_saves_the_projections_whole_or_not_at_all(lib):
     assert forward(lib, G=None) == rl.ERR_INVALID_ARG
     assert forward(lib, U=None) == rl.ERR_INVALID_ARG
+    assert forward(lib, low=None) == rl.ERR_INVALID_ARG
+    assert forward(lib, G=None, U=None) == rl.ERR_INVALID_ARG
     assert forward(lib, G=AT["G"] + 2) == rl.ERR_INVALID_ARG
 
 
@@ -80,13 +82,13 @@ def test_down_layer_is_checked_as_a_linear_layer(lib):
 
 
 SIZE = {"X": 2 * M * D, "Y": 2 * M * D, "dY": 2 * M * D, "dX": 2 * M * D, "G": 2 * M * F, "U": 2 * M * F,
-        "H": 2 * M * F, "W_gate": 2 * D * F, "W_up": 2 * D * F, "W_down": 2 * D * F, "dW_gate": 2 * D * F,
+        "low": 2 * M * F, "H": 2 * M * F, "W_gate": 2 * D * F, "W_up": 2 * D * F, "W_down": 2 * D * F, "dW_gate": 2 * D * F,
         "dW_up": 2 * D * F, "dW_down": 2 * D * F}
 
 
-@pytest.mark.parametrize("out", ["G", "U", "H", "Y"])
+@pytest.mark.parametrize("out", ["G", "U", "low", "H", "Y"])
 def test_forward_overlaps(lib, out):
-    for other in ("X", "W_gate", "W_up", "W_down", "G", "U", "H", "Y"):
+    for other in ("X", "W_gate", "W_up", "W_down", "G", "U", "low", "H", "Y"):
         if other != out:
             for at in (AT[other] + SIZE[other] - 16, AT[other] - SIZE[out] + 16):
                 assert forward(lib, **{out: at}) == rl.ERR_INVALID_ARG, other
@@ -102,7 +104,7 @@ def test_backward_overlaps(lib, out):
 
 
 def test_backward_pointers_and_workspace(lib):
-    for name in ("dY", "X", "W_gate", "W_up", "W_down", "G", "U", "H", "ws"):
+    for name in ("dY", "X", "W_gate", "W_up", "W_down", "G", "U", "low", "H", "ws"):
         assert backward(lib, **{name: None}) == rl.ERR_INVALID_ARG
     need = lib.rtlynx_gated_mlp_backward_workspace_size(M, D, F)
     assert backward(lib, ws_bytes=need - 1) == rl.ERR_INVALID_ARG
