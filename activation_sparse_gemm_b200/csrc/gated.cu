@@ -220,6 +220,45 @@ __device__ __forceinline__ void restore8(uint4 g, uint4 u, uint4 low, float* gf,
     }
 }
 
+__device__ __forceinline__ uint4 swap_lanes(uint4 v, int mask) {
+    return make_uint4(__shfl_xor_sync(0xFFFFFFFFu, v.x, mask), __shfl_xor_sync(0xFFFFFFFFu, v.y, mask),
+                      __shfl_xor_sync(0xFFFFFFFFu, v.z, mask), __shfl_xor_sync(0xFFFFFFFFu, v.w, mask));
+}
+
+// 32 columns of the lane's own row (row0 + lane) of a [rows, cols] array, zeros
+// outside it, in two steps.  Four lanes read 64 contiguous bytes of a row, eight
+// rows at a time, and a 4 x 4 exchange among them gives each its row: 16 bytes
+// from each of 32 rows at a time cost the load unit four times as much.
+__device__ __forceinline__ void load_rows32(const uint16_t* base, int row0, int col, int rows, int cols, uint4 (&v)[4]) {
+    const int lane = threadIdx.x & 31, u = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = row0 + (lane & ~3) + i, c = col + 8 * u;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (row < rows && c < cols) v[i] = __ldg(reinterpret_cast<const uint4*>(base + static_cast<size_t>(row) * cols + c));
+    }
+}
+
+__device__ __forceinline__ void own_row32(uint4 (&v)[4]) {
+    const int u = threadIdx.x & 3;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const uint4 got = swap_lanes(u & 1 ? v[i] : v[i + 1], 1);
+        if (u & 1)
+            v[i] = got;
+        else
+            v[i + 1] = got;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 got = swap_lanes(u & 2 ? v[i] : v[i + 2], 2);
+        if (u & 2)
+            v[i] = got;
+        else
+            v[i + 2] = got;
+    }
+}
+
 // TN: accumulator columns of a tile, half of them from either CTA's rows of B.
 template <int EPI, int ACT, int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -483,18 +522,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int c = c0; c < c0 + kCols; c += 32) {
                     uint32_t r[32];
                     uint4 gp[4], up[4], lp[4];
-                    const int col0 = w.nt * kTile + c, row = row0 + lane;
+                    const int col0 = w.nt * kTile + c;
                     if (row0 >= p.rows || col0 >= p.cols) break;  // the same in the whole warp
-                    const size_t at = static_cast<size_t>(row) * p.cols + col0;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        gp[q] = up[q] = lp[q] = make_uint4(0, 0, 0, 0);
-                        if (row < p.rows && col0 + 8 * q < p.cols) {
-                            gp[q] = __ldg(reinterpret_cast<const uint4*>(p.in[0] + at + 8 * q));
-                            up[q] = __ldg(reinterpret_cast<const uint4*>(p.in[1] + at + 8 * q));
-                            lp[q] = __ldg(reinterpret_cast<const uint4*>(p.in[2] + at + 8 * q));
-                        }
-                    }
+                    load_rows32(p.in[0], row0, col0, p.rows, p.cols, gp);
+                    load_rows32(p.in[1], row0, col0, p.rows, p.cols, up);
+                    load_rows32(p.in[2], row0, col0, p.rows, p.cols, lp);
+                    own_row32(gp);
+                    own_row32(up);
+                    own_row32(lp);
                     tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c), r);
                     tmem_ld_wait();
                     if (c + 32 >= c0 + kCols) release();
