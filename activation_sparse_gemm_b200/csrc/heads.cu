@@ -454,7 +454,9 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
 }
 
 // Adds the rows of partial sums: block (channel / 32, tensor); a warp takes
-// every eighth row, in order, then the warps' sums are added in order.
+// every 32nd row, in order, then the warps' sums are added in order.  (A row for
+// each of 148 SMs: five loads one after the other in each warp, not nineteen.)
+constexpr int kGradWarps = 32;
 struct WeightGradArgs {
     const float* part[2];
     float* dw[2];
@@ -462,21 +464,22 @@ struct WeightGradArgs {
     int dim;
 };
 
-__global__ void __launch_bounds__(kHeadThreads) rtlynx_heads_weight_grad_kernel(const WeightGradArgs args) {
-    __shared__ float sums[kHeadWarps][32];
+__global__ void __launch_bounds__(32 * kGradWarps) rtlynx_heads_weight_grad_kernel(const WeightGradArgs args) {
+    __shared__ float sums[kGradWarps][32];
     grid_dependency_wait();
+    launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.y, c = blockIdx.x * 32 + lane;
     if (!args.dw[t]) return;
     float total = 0.0f;
     if (c < args.dim)
-        for (uint32_t r = warp; r < args.rows[t]; r += kHeadWarps)
+        for (uint32_t r = warp; r < args.rows[t]; r += kGradWarps)
             total += args.part[t][static_cast<size_t>(r) * args.dim + c];
     sums[warp][lane] = total;
     __syncthreads();
     if (warp == 0 && c < args.dim) {
         float all = 0.0f;
-        for (int k = 0; k < kHeadWarps; ++k) all += sums[k][lane];
+        for (int k = 0; k < kGradWarps; ++k) all += sums[k][lane];
         args.dw[t][c] = all;
     }
 }
@@ -774,7 +777,7 @@ int run_heads(int kind, float sin_sign, const Call& call, int64_t B, int64_t S, 
             wg.dw[t] = call.dw[t];
             wg.rows[t] = args.t[t].blocks;
         }
-        e = launch_dependent(rtlynx_heads_weight_grad_kernel, dim3((D + 31) / 32, 2), dim3(kHeadThreads), 0, stream, wg);
+        e = launch_dependent(rtlynx_heads_weight_grad_kernel, dim3((D + 31) / 32, 2), dim3(32 * kGradWarps), 0, stream, wg);
         if (e) return RTLYNX_ERR_CUDA;
     }
     return RTLYNX_OK;
