@@ -245,7 +245,11 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
     // ahead 235, 80 registers 249); backward, with two tensors read and the weights' sums
     // kept, 128 and 16 warps, looking ahead (179 us when
     // measured; without 205, two heads 190).
-    constexpr int kUnroll = 4 / (sizeof(T) == 4 ? 2 : 1);
+    // Half pairing of a 16-bit type takes two loads for a lane's channels: two
+    // heads at a time backward (25286 tokens of 20 + 20 heads of 128: 154 us; four
+    // spill registers, 241 us).
+    constexpr bool kTwoLoads = HALF && sizeof(T) == 2;
+    constexpr int kUnroll = sizeof(T) == 4 || (kTwoLoads && KIND == kNormBackward) ? 2 : 4;
     constexpr int kGrads = KIND == kNormBackward ? kUnroll : 1;
     constexpr bool kPipe = KIND == kNormBackward;
     __shared__ double turns[kMaxPairs];
