@@ -608,13 +608,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-// Sums the partial tiles of a split problem in part order and rounds: a
-// thread owns eight columns of one row.  Grid: (tile * 2 + rank) x 16, with
-// 256 threads = 2 column octets x 128 rows.
-__global__ void __launch_bounds__(256) rtlynx_gated_sum_parts_kernel(const __grid_constant__ Problem p) {
+// Sums the partial tiles of the split problems in part order and rounds: a
+// thread owns eight columns of one row.  Grid: (tile * 2 + rank) x 16 x problem,
+// with 256 threads = 2 column octets x 128 rows.
+__global__ void __launch_bounds__(256) rtlynx_gated_sum_parts_kernel(const __grid_constant__ GatedArgs args) {
     grid_dependency_wait();
     launch_dependents();
+    const Problem& p = args.p[blockIdx.z];
     const int tile = blockIdx.x >> 1, rank = blockIdx.x & 1;
+    if (p.split <= 1 || tile >= p.m_pairs * p.n_tiles) return;
     const int row_in_cta = threadIdx.x & 127, octet = blockIdx.y * 2 + (threadIdx.x >> 7);
     int mp, nt;
     tile_at(p, tile, mp, nt);
@@ -644,8 +646,13 @@ int launch_gated(const GatedArgs& args, int num_sms, cudaStream_t stream) {
     return launch_dependent(kernel, dim3(2 * pairs), dim3(kThreads), kSmemBytes, stream, args);
 }
 
-int launch_sum_parts(const Problem& p, cudaStream_t stream) {
-    return launch_dependent(rtlynx_gated_sum_parts_kernel, dim3(p.m_pairs * p.n_tiles * 2, 16), dim3(256), 0, stream, p);
+// Follows a launch of the same arguments where it split anything.
+int launch_sum_parts(const GatedArgs& args, cudaStream_t stream) {
+    int tiles = 0;
+    for (int i = 0; i < args.problems; ++i)
+        if (args.p[i].split > 1 && args.p[i].m_pairs * args.p[i].n_tiles > tiles) tiles = args.p[i].m_pairs * args.p[i].n_tiles;
+    if (tiles == 0) return 0;
+    return launch_dependent(rtlynx_gated_sum_parts_kernel, dim3(2 * tiles, 16, args.problems), dim3(256), 0, stream, args);
 }
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
@@ -721,49 +728,77 @@ bool ranges_ok(const Range* in, int n_in, const Range* out, int n_out) {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-constexpr int kAssumedPairs = 74;  // sizes the workspace; a GPU with fewer pairs splits less
+// CTA pairs that the cutting along K reckons with (a B200's 148 SMs), whatever
+// the GPU, so that workspace sizes do not depend on it.
+constexpr int kPlanPairs = 74;
 
 // Stages' worth of time that a unit costs beside its stages (filling the
 // pipeline, its share of the epilogue).
 constexpr int kUnitCost = 4;
 
-// Most parts that the tiles of a [rows, cols] product are cut into along its
-// `stages` of K: where tiles are fewer than CTA pairs each pair gets at most
-// one part, of at least `least` stages.
-int most_parts(int64_t rows, int64_t cols, int64_t stages, int pairs, int least) {
-    const int64_t tiles = static_cast<int64_t>(ceil_div(rows, kTile)) * ceil_div(cols, kTile);
-    int64_t split = pairs / tiles;
-    if (split > stages / least) split = stages / least;
-    return static_cast<int>(split < 1 ? 1 : (split > 16 ? 16 : split));
-}
+size_t part_bytes(int64_t units) { return static_cast<size_t>(units) * kTile * kTile * sizeof(float); }
 
-size_t parts_bytes(int64_t rows, int64_t cols, int split) {
-    const size_t tiles = static_cast<size_t>(ceil_div(rows, kTile)) * ceil_div(cols, kTile);
-    return split > 1 ? tiles * split * kTile * kTile * sizeof(float) : 0;
+int64_t tiles_of(int64_t rows, int64_t cols) { return static_cast<int64_t>(ceil_div(rows, kTile)) * ceil_div(cols, kTile); }
+
+// Most parts that `tiles` of `stages` each are cut into along K: where they are
+// fewer than CTA pairs, each pair gets at most one part, of at least eight stages.
+int most_parts(int64_t tiles, int64_t stages) {
+    int64_t split = kPlanPairs / tiles;
+    if (split > stages / 8) split = stages / 8;
+    return static_cast<int>(split < 1 ? 1 : (split > 16 ? 16 : split));
 }
 
 // Y = H Wd^T of the forward call.  Parts of eight stages: at 1024 -> 2816 and
 // 64 tokens the call takes 19.7 us, 22.5 with parts of 16, 20.2 with parts of four.
-int down_parts(int64_t M, int64_t D, int64_t F, int pairs) {
-    return most_parts(M, D, ceil_div(F, 64), pairs < kAssumedPairs ? pairs : kAssumedPairs, 8);
-}
+int down_parts(int64_t M, int64_t D, int64_t F) { return most_parts(tiles_of(M, D), ceil_div(F, 64)); }
 
-// dX, K = 2 D_ff
-int dx_most_parts(int64_t M, int64_t D, int64_t F, int pairs) {
-    return most_parts(M, D, 2 * ceil_div(F, 64), pairs < kAssumedPairs ? pairs : kAssumedPairs, 8);
-}
+// How the second launch of the backward call is cut: dX has few long tiles
+// (K = 2 D_ff) with few tokens, the weights' gradients (K = tokens) with many
+// tokens and narrow weights.  Tiles are cut only while a part is longer than
+// what a CTA pair has to do on average.
+struct BackwardPlan {
+    int64_t x_tiles, x_stages, w_tiles, w_stages;  // of dX; of one weight's gradient
+    int x_split, w_split;
+    int64_t units;  // with fp32 partial tiles
 
+    BackwardPlan(int64_t M, int64_t D, int64_t F, bool x, int weights) {
+        x_tiles = x ? tiles_of(M, D) : 0;
+        x_stages = 2 * ceil_div(F, 64);
+        w_tiles = tiles_of(F, D);
+        w_stages = ceil_div(M, 64);
+        const int64_t w_all = weights * w_tiles;
+        const int64_t average = (x_tiles * (x_stages + kUnitCost) + w_all * (w_stages + kUnitCost)) / kPlanPairs + 1;
+        auto parts = [&](int64_t tiles, int64_t stages) {
+            if (tiles == 0) return 1;
+            const int64_t wanted = (stages + kUnitCost + average - 1) / average;
+            const int most = most_parts(tiles, stages);
+            return static_cast<int>(wanted < most ? wanted : most);
+        };
+        x_split = parts(x_tiles, x_stages);
+        w_split = parts(w_all, w_stages);
+        units = (x_split > 1 ? x_tiles * x_split : 0) + (w_split > 1 ? w_all * w_split : 0);
+    }
+    int64_t x_cost() const { return x_stages / x_split + kUnitCost; }  // of a unit
+    int64_t w_cost() const { return w_stages / w_split + kUnitCost; }
+};
 
 struct BackwardLayout {
     size_t dg, du, part, total;
 };
 
+// The workspace does for any choice of gradients.
 BackwardLayout backward_layout(int64_t M, int64_t D, int64_t F) {
     BackwardLayout l;
     l.dg = 0;
     l.du = align256(static_cast<size_t>(M) * F * 2);
     l.part = 2 * l.du;
-    l.total = l.part + parts_bytes(M, D, dx_most_parts(M, D, F, kAssumedPairs));
+    int64_t units = 0;
+    for (int x = 0; x < 2; ++x)
+        for (int weights = 0; weights < 4; ++weights) {
+            const int64_t u = BackwardPlan(M, D, F, x, weights).units;
+            if (u > units) units = u;
+        }
+    l.total = l.part + part_bytes(units);
     return l;
 }
 
@@ -776,7 +811,8 @@ extern "C" {
 
 size_t rtlynx_gated_mlp_block_workspace_size(int64_t M, int64_t D, int64_t D_ff, int mode_down) {
     if (check_sizes(M, D, D_ff, RTLYNX_ACT_SILU) || mode_down != RTLYNX_MODE_DENSE_SKIP || M <= kFewTokens) return 0;
-    return parts_bytes(M, D, down_parts(M, D, D_ff, kAssumedPairs));
+    const int split = down_parts(M, D, D_ff);
+    return split > 1 ? part_bytes(tiles_of(M, D) * split) : 0;
 }
 
 int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, const void* W_down,
@@ -867,7 +903,7 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
     Problem& p = args.p[0];
     p.m_pairs = ceil_div(M, kTile);
     p.n_tiles = ceil_div(D, kTile);
-    p.split = down_parts(M, D, D_ff, pairs);
+    p.split = down_parts(M, D, D_ff);
     p.part = static_cast<float*>(workspace);
     p.k0 = p.k = ceil_div(D_ff, 64);
     p.a0 = p.a1 = maps.add(H, M, D_ff, false);
@@ -880,7 +916,7 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
     p.cols = static_cast<int>(D);
     args.units = p.m_pairs * p.n_tiles * p.split;
     if (launch_gated<kStore, 0>(args, num_sms, stream)) return RTLYNX_ERR_CUDA;
-    return p.split > 1 && launch_sum_parts(p, stream) ? RTLYNX_ERR_CUDA : RTLYNX_OK;
+    return launch_sum_parts(args, stream) ? RTLYNX_ERR_CUDA : RTLYNX_OK;
 }
 
 size_t rtlynx_gated_mlp_backward_workspace_size(int64_t M, int64_t D, int64_t D_ff) {
@@ -959,13 +995,17 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         args.units += p.m_pairs * p.n_tiles * p.split;
         ++args.problems;
     };
-    // the weights' gradients: units of token_stages stages each
-    const int64_t w_tiles = static_cast<int64_t>(ceil_div(D_ff, kTile)) * ceil_div(D, kTile);
-    const int64_t shorts = w_tiles * ((dW_gate != nullptr) + (dW_up != nullptr) + (dW_down != nullptr));
-    const int64_t short_cost = token_stages + kUnitCost;
-    const bool has_dx = dX != nullptr;
-    if (has_dx) {
-        Problem& p = args.p[0];
+    const int weights = (dW_gate != nullptr) + (dW_up != nullptr) + (dW_down != nullptr);
+    const BackwardPlan plan(M, D, D_ff, dX != nullptr, weights);
+    float* part = reinterpret_cast<float*>(base + l.part);
+    auto parts_of = [&](Problem& p, int64_t tiles, int split) {
+        p.split = split;
+        p.part = part;
+        if (split > 1) part += part_bytes(tiles * split) / sizeof(float);
+    };
+    auto add_dx = [&]() {
+        if (!dX) return;
+        Problem& p = args.p[args.problems];
         p.k0 = ceil_div(D_ff, 64);
         p.k = 2 * p.k0;
         p.a0 = maps.add(dG, M, D_ff, false);
@@ -973,39 +1013,39 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         p.a1 = maps.add(dU, M, D_ff, false);
         p.b1 = maps.add(W_up, D_ff, D, true);
         p.b_mn = 1;
-        // cut only while a part is longer than what a CTA pair has to do on average
-        const int64_t tiles = static_cast<int64_t>(m_pairs) * ceil_div(D, kTile);
-        const int64_t average = (tiles * (p.k + kUnitCost) + shorts * short_cost) / pairs + 1;
-        const int64_t wanted = (p.k + kUnitCost + average - 1) / average;
-        const int most = dx_most_parts(M, D, D_ff, pairs);
-        p.split = static_cast<int>(wanted < most ? wanted : most);
-        p.part = reinterpret_cast<float*>(base + l.part);
+        parts_of(p, plan.x_tiles, plan.x_split);
         close(p, M, D, dX);
-        args.longs = args.units;
-        // see Units: short units that take as long as one dX unit
-        const int rest = args.longs % pairs;
-        if (rest > 0) {
-            int64_t extra = (p.k / p.split + kUnitCost) / short_cost;
-            const int64_t fair = (shorts + pairs - rest - 1) / (pairs - rest);
-            args.extra = static_cast<int>(extra < fair ? extra : fair);
-        }
-    }
+    };
     auto weight_grad = [&](const void* a, int64_t a_cols, const void* b, int64_t b_cols, void* out) {
+        if (!out) return;
         Problem& p = args.p[args.problems];
         p.k0 = p.k = token_stages;
         p.a0 = p.a1 = maps.add(a, M, a_cols, true);
         p.b0 = p.b1 = maps.add(b, M, b_cols, true);
         p.a_mn = p.b_mn = 1;
-        p.split = 1;
+        parts_of(p, plan.w_tiles, plan.w_split);
         close(p, a_cols, b_cols, out);
     };
-    if (dW_gate) weight_grad(dG, D_ff, X, D, dW_gate);
-    if (dW_up) weight_grad(dU, D_ff, X, D, dW_up);
-    if (dW_down) weight_grad(dY, D, H, D_ff, dW_down);
+    auto add_weights = [&]() {
+        weight_grad(dG, D_ff, X, D, dW_gate);
+        weight_grad(dU, D_ff, X, D, dW_up);
+        weight_grad(dY, D, H, D_ff, dW_down);
+    };
+    // The longer units first; see Units for what the pairs with one of them
+    // less take instead.
+    const bool x_first = plan.x_cost() >= plan.w_cost();
+    if (x_first) add_dx(); else add_weights();
+    args.longs = args.units;
+    if (x_first) add_weights(); else add_dx();
     if (!maps.ok) return RTLYNX_ERR_CUDA;
+    const int rest = args.longs % pairs;
+    if (rest > 0) {
+        const int64_t extra = x_first ? plan.x_cost() / plan.w_cost() : plan.w_cost() / plan.x_cost();
+        const int64_t fair = (args.units - args.longs + pairs - rest - 1) / (pairs - rest);
+        args.extra = static_cast<int>(extra < fair ? extra : fair);
+    }
     if (launch_gated<kStore, 0>(args, num_sms, stream)) return RTLYNX_ERR_CUDA;
-    if (has_dx && args.p[0].split > 1 && launch_sum_parts(args.p[0], stream)) return RTLYNX_ERR_CUDA;
-    return RTLYNX_OK;
+    return launch_sum_parts(args, stream) ? RTLYNX_ERR_CUDA : RTLYNX_OK;
 }
 
 }  // extern "C"

@@ -25,7 +25,7 @@ H_STEP = 2.0 ** -8
 
 SIZES = [(1, 8, 8), (1, 64, 136), (2, 1032, 264), (3, 72, 40), (5, 520, 1000), (8, 136, 264), (9, 2056, 552),
          (16, 256, 128), (17, 136, 264), (33, 264, 72), (64, 64, 64), (128, 256, 512), (129, 200, 328), (256, 512, 256),
-         (257, 520, 136), (300, 1032, 520), (700, 264, 1160), (1025, 72, 2056), (40, 264, 4104), (520, 136, 6152)]
+         (257, 520, 136), (300, 1032, 520), (700, 264, 1160), (1025, 72, 2056), (40, 264, 4104), (520, 136, 6152), (2900, 136, 72)]
 
 
 def ints(gen, shape, low, high, density):
