@@ -68,7 +68,7 @@ struct Problem {
     int a_mn, b_mn;             // operand is MN-major
     int rows, cols;             // of the output
     int out[4];                 // maps of the outputs; forward: H, G, U, low (the last three may be -1); backward: dG, dU
-    uint16_t* sum_out;          // split > 1: the output of the summing kernel
+    uint16_t* sum_out[2];       // split > 1: the outputs themselves, for the summing kernel
     const uint16_t* in[3];      // backward: G, U, low
     float* part;                // split > 1: fp32 partial tiles
 };
@@ -186,25 +186,19 @@ __device__ __forceinline__ void pack32(const uint32_t (&r)[32], uint4 (&v)[4]) {
     }
 }
 
-// The upper 16 bits of 32 values.
-__device__ __forceinline__ void high32(const uint32_t (&r)[32], uint4 (&v)[4]) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        v[q] = make_uint4(__byte_perm(r[8 * q], r[8 * q + 1], 0x7632), __byte_perm(r[8 * q + 2], r[8 * q + 3], 0x7632),
-                          __byte_perm(r[8 * q + 4], r[8 * q + 5], 0x7632), __byte_perm(r[8 * q + 6], r[8 * q + 7], 0x7632));
+// The upper 16 bits of eight values.
+__device__ __forceinline__ uint4 high8(const uint32_t* r) {
+    return make_uint4(__byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632), __byte_perm(r[4], r[5], 0x7632),
+                      __byte_perm(r[6], r[7], 0x7632));
 }
 
 // The eight bits below those, of two arrays: the first's in the low byte.
 __device__ __forceinline__ uint32_t low2(uint32_t a0, uint32_t b0, uint32_t a1, uint32_t b1) {
     return __byte_perm(__byte_perm(a0, b0, 0x0051), __byte_perm(a1, b1, 0x0051), 0x5410);
 }
-__device__ __forceinline__ void low32(const uint32_t (&a)[32], const uint32_t (&b)[32], uint4 (&v)[4]) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int j = 8 * q;
-        v[q] = make_uint4(low2(a[j], b[j], a[j + 1], b[j + 1]), low2(a[j + 2], b[j + 2], a[j + 3], b[j + 3]),
-                          low2(a[j + 4], b[j + 4], a[j + 5], b[j + 5]), low2(a[j + 6], b[j + 6], a[j + 7], b[j + 7]));
-    }
+__device__ __forceinline__ uint4 low8(const uint32_t* a, const uint32_t* b) {
+    return make_uint4(low2(a[0], b[0], a[1], b[1]), low2(a[2], b[2], a[3], b[3]), low2(a[4], b[4], a[5], b[5]),
+                      low2(a[6], b[6], a[7], b[7]));
 }
 
 // Eight values of G and U from their upper bits and the shared lower ones (the
@@ -218,6 +212,15 @@ __device__ __forceinline__ void restore8(uint4 g, uint4 u, uint4 low, float* gf,
         gf[2 * i + 1] = __uint_as_float(__byte_perm(gw[i], lw[i], 0x3266));
         uf[2 * i + 1] = __uint_as_float(__byte_perm(uw[i], lw[i], 0x3277));
     }
+}
+
+// dH with G and U, to dG and dU in their place.
+template <int ACT>
+__device__ __forceinline__ void gated_slopes(float dh, float& g, float& u) {
+    float value, slope;
+    act_both<ACT>(g, value, slope);
+    g = dh * u * slope;
+    u = dh * value;
 }
 
 __device__ __forceinline__ uint4 swap_lanes(uint4 v, int mask) {
@@ -507,11 +510,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     put(p.out[0], packed, col, row0);
                     if (p.out[1] >= 0) {
-                        high32(g, packed);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) packed[q] = high8(g + 8 * q);
                         put(p.out[1], packed, col, row0);
-                        high32(v, packed);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) packed[q] = high8(v + 8 * q);
                         put(p.out[2], packed, col, row0);
-                        low32(g, v, packed);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) packed[q] = low8(g + 8 * q, v + 8 * q);
                         put(p.out[3], packed, col, row0);
                     }
                 }
@@ -538,13 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         float gf[8], uf[8];
                         restore8(gp[q], up[q], lp[q], gf, uf);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float dh = __uint_as_float(r[8 * q + j]);
-                            float value, slope;
-                            act_both<ACT>(gf[j], value, slope);
-                            gf[j] = dh * uf[j] * slope;
-                            uf[j] = dh * value;
-                        }
+                        for (int j = 0; j < 8; ++j) gated_slopes<ACT>(__uint_as_float(r[8 * q + j]), gf[j], uf[j]);
                         gp[q] = pack8(gf);
                         up[q] = pack8(uf);
                     }
@@ -608,9 +608,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-// Sums the partial tiles of the split problems in part order and rounds: a
-// thread owns eight columns of one row.  Grid: (tile * 2 + rank) x 16 x problem,
-// with 256 threads = 2 column octets x 128 rows.
+// Eight columns of one row of a split tile, its parts added in order.
+__device__ __forceinline__ void sum_octet(const Problem& p, int tile, int rank, int row_in_cta, int octet, float (&sum)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+    for (int s = 0; s < p.split; ++s) {
+        const float4* src = reinterpret_cast<const float4*>(
+            p.part + ((static_cast<size_t>(tile) * p.split + s) * 2 + rank) * (kHalf * kTile));
+        const float4 a = src[(2 * octet) * kHalf + row_in_cta], b = src[(2 * octet + 1) * kHalf + row_in_cta];
+        sum[0] += a.x, sum[1] += a.y, sum[2] += a.z, sum[3] += a.w;
+        sum[4] += b.x, sum[5] += b.y, sum[6] += b.z, sum[7] += b.w;
+    }
+}
+
+// Sums the partial tiles of the split problems, and takes dH on to dG and dU
+// where it is that (EPI kGatedBackward): a thread owns eight columns of one row.
+// Grid: (tile * 2 + rank) x 16 x problem, with 256 threads = 2 column octets x
+// 128 rows.
+template <int EPI, int ACT>
 __global__ void __launch_bounds__(256) rtlynx_gated_sum_parts_kernel(const __grid_constant__ GatedArgs args) {
     grid_dependency_wait();
     launch_dependents();
@@ -623,20 +638,26 @@ __global__ void __launch_bounds__(256) rtlynx_gated_sum_parts_kernel(const __gri
     const int row = mp * kTile + rank * kHalf + row_in_cta;
     const int col = nt * kTile + 8 * octet;
     if (row >= p.rows || col >= p.cols) return;
-    float sum[8] = {};
-    for (int s = 0; s < p.split; ++s) {
-        const float4* src = reinterpret_cast<const float4*>(
-            p.part + ((static_cast<size_t>(tile) * p.split + s) * 2 + rank) * (kHalf * kTile));
-        const float4 a = src[(2 * octet) * kHalf + row_in_cta], b = src[(2 * octet + 1) * kHalf + row_in_cta];
-        sum[0] += a.x, sum[1] += a.y, sum[2] += a.z, sum[3] += a.w;
-        sum[4] += b.x, sum[5] += b.y, sum[6] += b.z, sum[7] += b.w;
+    const size_t at = static_cast<size_t>(row) * p.cols + col;
+    auto write = [&](int i, uint4 v) { *reinterpret_cast<uint4*>(p.sum_out[i] + at) = v; };
+    float f[8];
+    sum_octet(p, tile, rank, row_in_cta, octet, f);
+    if constexpr (EPI == kStore) {
+        write(0, pack8(f));
+    } else {
+        auto read = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(p.in[i] + at)); };
+        float g[8], u[8];
+        restore8(read(0), read(1), read(2), g, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) gated_slopes<ACT>(f[j], g[j], u[j]);
+        write(0, pack8(g));
+        write(1, pack8(u));
     }
-    *reinterpret_cast<uint4*>(p.sum_out + static_cast<size_t>(row) * p.cols + col) = pack8(sum);
 }
 
 // ---------------------------------------------------------------- host side
-template <int EPI, int ACT, int TN = kTile>
-int launch_gated(const GatedArgs& args, int num_sms, cudaStream_t stream) {
+template <int EPI, int ACT, int TN>
+int launch_tiles(const GatedArgs& args, int num_sms, cudaStream_t stream) {
     auto kernel = rtlynx_gated_gemm_kernel<EPI, ACT, TN>;
     static std::atomic<uint64_t> smem_set{0};
     const int e = allow_max_dynamic_smem(kernel, smem_set);
@@ -646,13 +667,19 @@ int launch_gated(const GatedArgs& args, int num_sms, cudaStream_t stream) {
     return launch_dependent(kernel, dim3(2 * pairs), dim3(kThreads), kSmemBytes, stream, args);
 }
 
-// Follows a launch of the same arguments where it split anything.
-int launch_sum_parts(const GatedArgs& args, cudaStream_t stream) {
+// The tiled kernel; where anything was split, the plain one, whose units
+// leave partial tiles, and the sums with the epilogue asked for.
+template <int EPI, int ACT, int TN = kTile>
+int launch_gated(const GatedArgs& args, int num_sms, cudaStream_t stream) {
     int tiles = 0;
     for (int i = 0; i < args.problems; ++i)
         if (args.p[i].split > 1 && args.p[i].m_pairs * args.p[i].n_tiles > tiles) tiles = args.p[i].m_pairs * args.p[i].n_tiles;
-    if (tiles == 0) return 0;
-    return launch_dependent(rtlynx_gated_sum_parts_kernel, dim3(2 * tiles, 16, args.problems), dim3(256), 0, stream, args);
+    if (EPI == kGatedForward || tiles == 0) return launch_tiles<EPI, ACT, TN>(args, num_sms, stream);
+    const int e = launch_tiles<kStore, 0, kTile>(args, num_sms, stream);
+    if (e) return e;
+    constexpr int kSum = EPI == kGatedForward ? kStore : EPI;
+    return launch_dependent(rtlynx_gated_sum_parts_kernel<kSum, ACT>, dim3(2 * tiles, 16, args.problems), dim3(256), 0,
+                            stream, args);
 }
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
@@ -752,6 +779,15 @@ int most_parts(int64_t tiles, int64_t stages) {
 // 64 tokens the call takes 19.7 us, 22.5 with parts of 16, 20.2 with parts of four.
 int down_parts(int64_t M, int64_t D, int64_t F) { return most_parts(tiles_of(M, D), ceil_div(F, 64)); }
 
+// dH = dY Wd, where that saves more than the extra kernel costs: at 95 tokens and
+// 2472 -> 864 its four tiles have 39 stages each (training step 50 us, 68 with the
+// tiles whole).  The gate and up projections are not cut: it made 957 tokens at
+// 2000 -> 784 take 25.9 us instead of 20.9, and gained nothing elsewhere.
+int dh_parts(int64_t M, int64_t D, int64_t F) {
+    const int64_t stages = ceil_div(D, 64);
+    return stages < 32 ? 1 : most_parts(tiles_of(M, F), stages);
+}
+
 // How the second launch of the backward call is cut: dX has few long tiles
 // (K = 2 D_ff) with few tokens, the weights' gradients (K = tokens) with many
 // tokens and narrow weights.  Tiles are cut only while a part is longer than
@@ -793,6 +829,8 @@ BackwardLayout backward_layout(int64_t M, int64_t D, int64_t F) {
     l.du = align256(static_cast<size_t>(M) * F * 2);
     l.part = 2 * l.du;
     int64_t units = 0;
+    const int dh = dh_parts(M, D, F);
+    if (dh > 1) units = tiles_of(M, F) * dh;
     for (int x = 0; x < 2; ++x)
         for (int weights = 0; weights < 4; ++weights) {
             const int64_t u = BackwardPlan(M, D, F, x, weights).units;
@@ -810,7 +848,8 @@ using namespace rtlynx;
 extern "C" {
 
 size_t rtlynx_gated_mlp_block_workspace_size(int64_t M, int64_t D, int64_t D_ff, int mode_down) {
-    if (check_sizes(M, D, D_ff, RTLYNX_ACT_SILU) || mode_down != RTLYNX_MODE_DENSE_SKIP || M <= kFewTokens) return 0;
+    if (check_sizes(M, D, D_ff, RTLYNX_ACT_SILU) || M <= kFewTokens) return 0;
+    if (mode_down != RTLYNX_MODE_DENSE_SKIP) return 0;
     const int split = down_parts(M, D, D_ff);
     return split > 1 ? part_bytes(tiles_of(M, D) * split) : 0;
 }
@@ -909,14 +948,13 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
     p.a0 = p.a1 = maps.add(H, M, D_ff, false);
     p.b0 = p.b1 = maps.add(W_down, D, D_ff, false);
     p.out[0] = maps.out(Y, M, D);
-    p.sum_out = static_cast<uint16_t*>(Y);
+    p.sum_out[0] = static_cast<uint16_t*>(Y);
     if (!maps.ok) return RTLYNX_ERR_CUDA;
     p.group_n = raster_group(p, pairs);
     p.rows = static_cast<int>(M);
     p.cols = static_cast<int>(D);
     args.units = p.m_pairs * p.n_tiles * p.split;
-    if (launch_gated<kStore, 0>(args, num_sms, stream)) return RTLYNX_ERR_CUDA;
-    return launch_sum_parts(args, stream) ? RTLYNX_ERR_CUDA : RTLYNX_OK;
+    return launch_gated<kStore, 0>(args, num_sms, stream) ? RTLYNX_ERR_CUDA : RTLYNX_OK;
 }
 
 size_t rtlynx_gated_mlp_backward_workspace_size(int64_t M, int64_t D, int64_t D_ff) {
@@ -959,13 +997,16 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         Problem& p = args.p[0];
         p.m_pairs = m_pairs;
         p.n_tiles = ceil_div(D_ff, kTile);
-        p.split = 1;
+        p.split = dh_parts(M, D, D_ff);
+        p.part = reinterpret_cast<float*>(base + l.part);
         p.k0 = p.k = ceil_div(D, 64);
         p.a0 = p.a1 = maps.add(dY, M, D, false);
         p.b0 = p.b1 = maps.add(W_down, D, D_ff, true);
         p.b_mn = 1;
         p.out[0] = maps.out(dG, M, D_ff);
         p.out[1] = maps.out(dU, M, D_ff);
+        p.sum_out[0] = dG;
+        p.sum_out[1] = dU;
         if (!maps.ok) return RTLYNX_ERR_CUDA;
         p.group_n = raster_group(p, num_sms / 2);
         p.rows = static_cast<int>(M);
@@ -973,7 +1014,7 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         p.in[0] = static_cast<const uint16_t*>(G);
         p.in[1] = static_cast<const uint16_t*>(U);
         p.in[2] = static_cast<const uint16_t*>(low);
-        args.units = p.m_pairs * p.n_tiles;
+        args.units = p.m_pairs * p.n_tiles * p.split;
         const int e = act == RTLYNX_ACT_SILU ? launch_gated<kGatedBackward, RTLYNX_ACT_SILU>(args, num_sms, stream)
                                              : launch_gated<kGatedBackward, RTLYNX_ACT_GELU>(args, num_sms, stream);
         if (e) return RTLYNX_ERR_CUDA;
@@ -989,7 +1030,7 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         p.rows = static_cast<int>(rows);
         p.cols = static_cast<int>(cols);
         p.out[0] = maps.out(out, rows, cols);
-        p.sum_out = static_cast<uint16_t*>(out);
+        p.sum_out[0] = static_cast<uint16_t*>(out);
         p.group_n = raster_group(p, pairs);
         p.first_unit = args.units;
         args.units += p.m_pairs * p.n_tiles * p.split;
@@ -1044,8 +1085,7 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         const int64_t fair = (args.units - args.longs + pairs - rest - 1) / (pairs - rest);
         args.extra = static_cast<int>(extra < fair ? extra : fair);
     }
-    if (launch_gated<kStore, 0>(args, num_sms, stream)) return RTLYNX_ERR_CUDA;
-    return launch_sum_parts(args, stream) ? RTLYNX_ERR_CUDA : RTLYNX_OK;
+    return launch_gated<kStore, 0>(args, num_sms, stream) ? RTLYNX_ERR_CUDA : RTLYNX_OK;
 }
 
 }  // extern "C"

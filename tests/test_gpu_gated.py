@@ -25,7 +25,8 @@ H_STEP = 2.0 ** -8
 
 SIZES = [(1, 8, 8), (1, 64, 136), (2, 1032, 264), (3, 72, 40), (5, 520, 1000), (8, 136, 264), (9, 2056, 552),
          (16, 256, 128), (17, 136, 264), (33, 264, 72), (64, 64, 64), (128, 256, 512), (129, 200, 328), (256, 512, 256),
-         (257, 520, 136), (300, 1032, 520), (700, 264, 1160), (1025, 72, 2056), (40, 264, 4104), (520, 136, 6152), (2900, 136, 72)]
+         (257, 520, 136), (300, 1032, 520), (700, 264, 1160), (1025, 72, 2056), (40, 264, 4104), (520, 136, 6152), (2900, 136, 72),
+         (30, 2056, 264), (270, 2312, 520)]
 
 
 def ints(gen, shape, low, high, density):
@@ -146,7 +147,7 @@ def check_normal(got, ref, K, what):
 
 @pytest.mark.parametrize("act", [rl.ACT_SILU, rl.ACT_GELU])
 @pytest.mark.parametrize("size", [(1, 520, 1288), (4, 2056, 776), (13, 264, 1032), (40, 1032, 392), (300, 520, 1160),
-                                  (1100, 776, 2056)], ids=str)
+                                  (1100, 776, 2056), (50, 2312, 776)], ids=str)
 def test_normal_inputs(size, act):
     M, D, F = size
     gen = torch.Generator(device="cuda").manual_seed(M)
@@ -237,10 +238,10 @@ def test_saturated_rows_and_nan_stay_in_their_row():
 
 
 @pytest.mark.parametrize("act", [rl.ACT_SILU, rl.ACT_GELU])
-@pytest.mark.parametrize("M", [1, 12, 200])
-def test_sparse_down_projection(act, M):
+@pytest.mark.parametrize("M,D", [(1, 264), (12, 264), (200, 264), (40, 2056)])
+def test_sparse_down_projection(act, M, D):
     """mode_down = sparse runs the same layer as rl.linear on the same H."""
-    D, F, R = 264, 520, 16
+    F, R = 520, 16
     gen = torch.Generator(device="cuda").manual_seed(M)
     def new(*shape, scale=1.0):
         return (scale * torch.randn(*shape, device="cuda", generator=gen)).bfloat16()
@@ -251,9 +252,8 @@ def test_sparse_down_projection(act, M):
         assert torch.equal(y, rl.linear(H, W[2], la, lb, mode=rl.MODE_SPARSE))
 
 
-@pytest.mark.parametrize("M", [1, 9, 140])
-def test_other_stream_and_captured_graph(M):
-    D, F = 264, 520
+@pytest.mark.parametrize("M,D,F", [(1, 264, 520), (9, 264, 520), (140, 264, 520), (140, 2056, 4104)])
+def test_other_stream_and_captured_graph(M, D, F):
     gen = torch.Generator(device="cuda").manual_seed(3)
     def new(*shape):
         return torch.randn(*shape, device="cuda", generator=gen).bfloat16()
@@ -291,7 +291,7 @@ def test_other_stream_and_captured_graph(M):
     assert rl.rtlynx_stream_status() == rl.OK
 
 
-@pytest.mark.parametrize("size", [(5, 72, 136), (150, 136, 264), (70, 136, 4104)], ids=str)
+@pytest.mark.parametrize("size", [(5, 72, 136), (150, 136, 264), (70, 136, 4104), (70, 2056, 136)], ids=str)
 def test_nothing_else_is_written(size):
     """Guard rows around every output stay as they were."""
     M, D, F = size
