@@ -412,15 +412,21 @@ class Rope:
             raise ValueError(f"one to {MAX_AXES} axes, got {len(self.axes)}")
         if any(a < 2 or a % 2 for a in self.axes):
             raise ValueError(f"every axis has an even number of channels, got {self.axes}")
-        self._freq = None
-        if inv_freq is not None:
+        pairs = sum(self.axes) // 2
+        if inv_freq is None:
+            theta = float(theta)
+            if not 0.0 < theta < float("inf"):
+                raise ValueError(f"theta is positive and finite, got {theta}")
+            values = [theta ** (-2.0 * j / n) for n in self.axes for j in range(n // 2)]
+        else:
             values = [float(v) for v in inv_freq]
-            if len(values) != sum(self.axes) // 2:
-                raise ValueError(f"inv_freq has {len(values)} values, the axes {sum(self.axes) // 2} pairs")
-            self._freq = (ctypes.c_double * len(values))(*values)
+            if len(values) != pairs:
+                raise ValueError(f"inv_freq has {len(values)} values, the axes {pairs} pairs")
+        # the calls read the frequencies from here, so no call has to raise theta to 64 powers
+        self._freq = (ctypes.c_double * pairs)(*values)
         dims = (ctypes.c_int32 * MAX_AXES)(*self.axes)
-        freq = ctypes.cast(self._freq, ctypes.POINTER(ctypes.c_double)) if self._freq is not None else None
-        self.specs = tuple(RopeSpec(len(self.axes), dims, int(pairing), t, float(theta), freq)
+        freq = ctypes.cast(self._freq, ctypes.POINTER(ctypes.c_double))
+        self.specs = tuple(RopeSpec(len(self.axes), dims, int(pairing), t, 0.0, freq)
                            for t in (POS_INT32, POS_INT64, POS_FP32))
 
 
@@ -642,7 +648,7 @@ def gated_mlp_backward(dY, X, W_gate, W_up, W_down, saved, act=ACT_SILU, needs=(
             for t, name in zip(saved, ("G", "U", "low", "H"), strict=True)]
     handle, ctx = _launch_on(device, stream)
     with ctx:
-        grads = tuple(torch.empty_like(t) if need else None for t, need in zip((X, W_gate, W_up, W_down), needs))
+        grads = tuple(torch.empty_like(t) if need else None for t, need in zip((X, W_gate, W_up, W_down), needs, strict=True))
         ws_bytes = rtlynx_gated_mlp_backward_workspace_size(M, D, F)
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
         status = lib().rtlynx_gated_mlp_backward(dy, *at, *kept, *(_ptr(g) for g in grads), M, D, F, act,

@@ -1,18 +1,30 @@
 // Gated feed-forward block for sm_100a, forward and backward.
 //
 //   G = X Wg^T,  U = X Wu^T,  H = act(G) * U        one kernel
-//   Y = H Wd^T                                      the linear layer (gemm.cu)
+//   Y = H Wd^T                                      one kernel (or a sparse layer)
 //   backward:
 //   dH = dY Wd,  dG = dH U act'(G),  dU = dH act(G) one kernel
 //   dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X,  dWd = dY^T H
 //                                                   one kernel for all four
 //
-// All of it is GEMM work, bound by the tensor cores but for few tokens.  One
-// persistent kernel template serves the three launches: a CTA pair computes
-// 256 x 256 of fp32 accumulator with cta_group::2 MMAs, each CTA holding 128
-// rows of A and 128 of B, with the accumulator double-buffered in tensor
-// memory so that the epilogue of one tile overlaps the main loop of the next.
-// Warp 0 loads by TMA, warp 1 issues the MMAs, the others run the epilogue.
+// All of it is GEMM work, bound by the tensor cores but for few tokens (up to
+// 16: gated_few.cu).  One persistent kernel template serves the four launches:
+// a CTA pair computes 256 x 256 of fp32 accumulator with cta_group::2 MMAs, each
+// CTA holding 128 rows of A and 128 of B, with the accumulator double-buffered
+// in tensor memory so that the epilogue of one tile overlaps the main loop of
+// the next.  Warp 0 loads by TMA, warp 1 issues the MMAs, the others run the
+// epilogue.  Where tiles are fewer than CTA pairs and long, they are cut along
+// K; the parts are left in fp32 in the caller's workspace, and a small kernel
+// adds them in order.
+//
+// Measured, TFLOP/s of the call (the measured cuBLAS rate is 1632 in a burst and
+// 1354 under the power cap): forward at 32760 x 5120 -> 13824 1370-1570 by the
+// power state, training step on 8192 tokens 1270-1530.  Tensor pipe active
+// 85% (gate and up), 78% (down), 79% (dH) and 86% (gradients) at 4096 tokens.
+// A stage's operands are 32 KB a CTA for 512 cycles of MMAs, so L2 has to deliver
+// 64 bytes a cycle to every SM: rows that do not start on 128-byte lines (widths
+// not a multiple of 64) stretch a stage to about 700 cycles.  With D below about 512
+// the epilogue outlasts the main loop.
 //
 // Gate and up projections in one kernel: CTA 0's half of B is 128 rows of Wg,
 // CTA 1's the same 128 rows of Wu.  The pair's MMA then leaves G in columns
@@ -59,7 +71,8 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 enum Epilogue { kStore = 0, kGatedForward = 1, kGatedBackward = 2 };
 
 // One product A B^T (+ A' B'^T) of a launch.  Map indices point into
-// GatedArgs::maps; with b_by_rank CTA 1 uses the map after b0.
+// GatedArgs::maps; going forward CTA 0 reads B through map b0 (Wg) and CTA 1
+// through the next one (Wu).
 struct Problem {
     int m_pairs, n_tiles, group_n;
     int first_unit, split;      // units [first_unit, first_unit + tiles * split)
@@ -96,11 +109,11 @@ __device__ __forceinline__ void tile_at(const Problem& p, int tile, int& mp, int
     nt = g * p.group_n + in_group - mp * width;
 }
 
-// The units of a CTA pair, one after another.  The first `longs` units (dX,
-// whose K is 2 D_ff) are dealt round; the pairs from `rest` on, which have one of
-// them less, take `extra` of the others each instead, and what is left is
-// dealt round.  Divisions are kept out of the way of the common case (nothing
-// split, no long units): every role computes this between two tiles.
+// The units of a CTA pair, one after another.  The first `longs` units (the
+// longer kind where a launch has two) are dealt round; the pairs from `rest` on,
+// which have one of them less, take `extra` of the others each instead, and what
+// is left is dealt round.  Divisions are kept out of the way of the common case
+// (nothing split, no long units): every role computes this between two tiles.
 struct Units {
     int pair, pairs, rest, own, shift;
 
@@ -450,8 +463,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
         // A lane has 32 columns of its own row: they go out as 32 x 32 pieces
         // through shared memory (64B swizzle) and TMA, which clips the ragged
-        // edges.  Stored straight from the lanes, 16 bytes to each of 32 rows at
-        // a time, outputs with a short K take twice as long.
+        // edges.  (Training step on 64 tokens at 5120 -> 13824, whose weights'
+        // gradients are all output: 319 us; 478 with 16 bytes to each of 32 rows
+        // at a time straight from the lanes, 372 with rows exchanged through
+        // shared memory and plain stores.)
         uint8_t* piece = pieces + (warp - 2) * 2 * kPieceBytes;
         int turn = 0;
         auto put = [&](int map, const uint4 (&v)[4], int col, int row) {
@@ -775,8 +790,9 @@ int most_parts(int64_t tiles, int64_t stages) {
     return static_cast<int>(split < 1 ? 1 : (split > 16 ? 16 : split));
 }
 
-// Y = H Wd^T of the forward call.  Parts of eight stages: at 1024 -> 2816 and
-// 64 tokens the call takes 19.7 us, 22.5 with parts of 16, 20.2 with parts of four.
+// Y = H Wd^T of the forward call: 64 tokens at 5120 -> 13824 take 93 us, 123 with
+// the tiles whole.  Parts of eight stages: at 1024 -> 2816 and 64 tokens the call
+// takes 19.7 us, 22.5 with parts of 16, 20.2 with parts of four.
 int down_parts(int64_t M, int64_t D, int64_t F) { return most_parts(tiles_of(M, D), ceil_div(F, 64)); }
 
 // dH = dY Wd, where that saves more than the extra kernel costs: at 95 tokens and
@@ -905,6 +921,9 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
         // Tiles of 64 output columns where rounds of them over the pairs end
         // sooner than rounds of 128: with few tokens, 13824 columns are 108
         // tiles for 74 pairs (two rounds) or 216 (three of half the length).
+        // 64 tokens at 5120 -> 13824: 92.6 us, 96.7 wide; 128 at 256 -> 512: 12.3
+        // and 14.1.  Past four rounds wide tiles win by reading X half as
+        // often (900 at 2048 -> 8192: 81 us, 88 narrow).
         const int64_t wide = static_cast<int64_t>(p.m_pairs) * ceil_div(D_ff, kHalf);
         const int64_t thin = static_cast<int64_t>(p.m_pairs) * ceil_div(D_ff, kNarrow / 2);
         const bool narrow = thin <= 4ll * pairs && ceil_div(thin, pairs) < 2 * ceil_div(wide, pairs);
