@@ -7,8 +7,8 @@
 //   dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X,  dWd = dY^T H
 //                                                   one kernel for all four
 //
-// All of it is GEMM work, bound by the tensor cores but for few tokens (up to
-// 16: gated_few.cu).  One persistent kernel template serves the four launches:
+// All of it is GEMM work, bound by the tensor cores but for few tokens, which
+// have kernels of their own going forward (gated_few.cu, gated_some.cu).  One persistent kernel template serves the four launches:
 // a CTA pair computes 256 x 256 of fp32 accumulator with cta_group::2 MMAs, each
 // CTA holding 128 rows of A and 128 of B, with the accumulator double-buffered
 // in tensor memory so that the epilogue of one tile overlaps the main loop of
@@ -790,10 +790,24 @@ int most_parts(int64_t tiles, int64_t stages) {
     return static_cast<int>(split < 1 ? 1 : (split > 16 ? 16 : split));
 }
 
-// Y = H Wd^T of the forward call: 64 tokens at 5120 -> 13824 take 93 us, 123 with
-// the tiles whole.  Parts of eight stages: at 1024 -> 2816 and 64 tokens the call
-// takes 19.7 us, 22.5 with parts of 16, 20.2 with parts of four.
+// Y = H Wd^T of the forward call, past gated_some.cu's tokens: 1500 at 512 -> 5632
+// take 44.1 us, 53.9 with the tiles whole.  (Parts of eight stages, measured
+// with 64 tokens at 1024 -> 2816: 19.7 us, 22.5 with parts of 16, 20.2 with
+// parts of four.)
 int down_parts(int64_t M, int64_t D, int64_t F) { return most_parts(tiles_of(M, D), ceil_div(F, 64)); }
+
+// Which kernels run the forward call.  Up to 8 tokens those of gated_few.cu; up
+// to 16 too, but with weights past 128 MB those of gated_some.cu (16 tokens at
+// 5120 -> 13824: 73 us against 90; at 4096 -> 11008 53 and 70; but at 2048 -> 5632
+// 24.4 against 22.8).  Up to 128 tokens gated_some.cu's down-projection (64 at
+// 5120 -> 13824: 88 us against 97 for the call, 128 at 256 -> 512: 11.2 and 11.7;
+// at 256 tokens 115 and 113), and its gate and up projections where there are
+// enough tiles of 128 channels for the SMs, and the more the more tokens: half
+// of 3 / 2 a token (64 at 5120 -> 13824: 77 us against 88, at 2048 -> 5632 27.9 and
+// 28.3, at 1024 -> 2816 18.4 against 16.4).
+bool few_kernels(int64_t M, int64_t D, int64_t F) { return M <= 8 || (M <= kFewTokens && 6 * D * F <= 128000000); }
+bool some_down(int64_t M) { return M <= kSomeTokens; }
+bool some_gate(int64_t M, int64_t F) { return M <= kSomeTokens && 2 * M <= 3 * ceil_div(F, 128); }
 
 // dH = dY Wd, where that saves more than the extra kernel costs: at 95 tokens and
 // 2472 -> 864 its four tiles have 39 stages each (training step 50 us, 68 with the
@@ -864,8 +878,12 @@ using namespace rtlynx;
 extern "C" {
 
 size_t rtlynx_gated_mlp_block_workspace_size(int64_t M, int64_t D, int64_t D_ff, int mode_down) {
-    if (check_sizes(M, D, D_ff, RTLYNX_ACT_SILU) || M <= kFewTokens) return 0;
+    if (check_sizes(M, D, D_ff, RTLYNX_ACT_SILU) || few_kernels(M, D, D_ff)) return 0;
     if (mode_down != RTLYNX_MODE_DENSE_SKIP) return 0;
+    if (some_down(M)) {
+        const int split = down_some_parts(D, D_ff);
+        return split > 1 ? align256(static_cast<size_t>(split) * M * D * sizeof(float)) : 0;
+    }
     const int split = down_parts(M, D, D_ff);
     return split > 1 ? part_bytes(tiles_of(M, D) * split) : 0;
 }
@@ -901,7 +919,7 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
     if (rc) return rc;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     const int pairs = num_sms / 2;
-    if (M <= kFewTokens) {
+    if (few_kernels(M, D, D_ff)) {
         if (launch_gated_few(X, W_gate, W_up, H, G, U, low, static_cast<int>(M), static_cast<int>(D),
                              static_cast<int>(D_ff), act, stream))
             return RTLYNX_ERR_CUDA;
@@ -911,7 +929,9 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
                    ? RTLYNX_ERR_CUDA
                    : RTLYNX_OK;
     }
-    {
+    if (some_gate(M, D_ff)) {
+        if (launch_gated_some(X, W_gate, W_up, H, G, U, low, M, D, D_ff, act, err, stream)) return RTLYNX_ERR_CUDA;
+    } else {
         GatedArgs args{};
         Maps maps{args};
         args.problems = 1;
@@ -919,10 +939,10 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
         Problem& p = args.p[0];
         p.m_pairs = ceil_div(M, kTile);
         // Tiles of 64 output columns where rounds of them over the pairs end
-        // sooner than rounds of 128: with few tokens, 13824 columns are 108
+        // sooner than rounds of 128: with 200 tokens, 13824 columns are 108
         // tiles for 74 pairs (two rounds) or 216 (three of half the length).
-        // 64 tokens at 5120 -> 13824: 92.6 us, 96.7 wide; 128 at 256 -> 512: 12.3
-        // and 14.1.  Past four rounds wide tiles win by reading X half as
+        // 128 tokens at 256 -> 512: 12.3 us, 14.1 wide; 64 at 5120 -> 13824 (before
+        // they had kernels of their own) 92.6 and 96.7.  Past four rounds wide tiles win by reading X half as
         // often (900 at 2048 -> 8192: 81 us, 88 narrow).
         const int64_t wide = static_cast<int64_t>(p.m_pairs) * ceil_div(D_ff, kHalf);
         const int64_t thin = static_cast<int64_t>(p.m_pairs) * ceil_div(D_ff, kNarrow / 2);
@@ -954,6 +974,9 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
     }
     if (mode_down == RTLYNX_MODE_SPARSE)
         return rtlynx_linear(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down, stream_);
+    if (some_down(M))
+        return launch_down_some(H, W_down, Y, static_cast<float*>(workspace), M, D_ff, D, err, stream) ? RTLYNX_ERR_CUDA
+                                                                                                       : RTLYNX_OK;
     GatedArgs args{};
     Maps maps{args};
     args.problems = 1;

@@ -18,10 +18,9 @@
 // The warps' fp32 sums meet in shared memory and are added in warp order.
 //
 // Measured at D = 5120, D_ff = 13824 (424.7 MB of weights, 64.9 us at the
-// measured copy rate): 1 token 70.7 us (6.0 TB/s), 8 tokens 75.2, 16 tokens 90.6;
-// the many-token kernel takes 145, 138 and 129.  From 17 tokens on it wins there
-// (129 against 134): a block re-reads the tokens from L2 as often as it reads
-// weights.
+// measured copy rate): 1 token 70 us (6.0 TB/s), 8 tokens 74; 16 tokens 88, as a
+// block re-reads the tokens from L2 half as often as it reads weights, which is
+// where gated_some.cu takes over.  11 tokens at 2056 -> 5512: 19 us.
 #include "../../include/rtlynx.h"
 #include "act.cuh"
 #include "internal.h"
