@@ -942,8 +942,9 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
         // sooner than rounds of 128: with 200 tokens, 13824 columns are 108
         // tiles for 74 pairs (two rounds) or 216 (three of half the length).
         // 128 tokens at 256 -> 512: 12.3 us, 14.1 wide; 64 at 5120 -> 13824 (before
-        // they had kernels of their own) 92.6 and 96.7.  Past four rounds wide tiles win by reading X half as
-        // often (900 at 2048 -> 8192: 81 us, 88 narrow).
+        // they had kernels of their own) 92.6 and 96.7.  Past four rounds wide
+        // tiles win by reading X half as often (900 at 2048 -> 8192: 81 us, 88
+        // narrow).
         const int64_t wide = static_cast<int64_t>(p.m_pairs) * ceil_div(D_ff, kHalf);
         const int64_t thin = static_cast<int64_t>(p.m_pairs) * ceil_div(D_ff, kNarrow / 2);
         const bool narrow = thin <= 4ll * pairs && ceil_div(thin, pairs) < 2 * ceil_div(wide, pairs);

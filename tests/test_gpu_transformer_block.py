@@ -113,3 +113,52 @@ def test_block_forward_and_backward(S, H, Hk, d, F, axes):
     for got, want, name in zip(d_ff[1:], grads[1:4], names):
         close(got, want, 12, "d" + name)
     assert rl.rtlynx_stream_status() == rl.OK
+
+
+@pytest.mark.parametrize("M", [1, 12, 60, 200])
+def test_forked_and_joined_streams_in_a_graph(M):
+    """Calls on two streams that fork and join inside a captured graph, behind copies, replayed with new inputs: the
+    kernels' early launches may not outrun what they read, weights included."""
+    D, F, H, d = 264, 4104, 3, 88
+    gen = torch.Generator(device="cuda").manual_seed(M)
+
+    def new(*shape, scale=1.0):
+        return (scale * torch.randn(*shape, device="cuda", generator=gen)).bfloat16()
+
+    fresh = [new(M, D), new(F, D, scale=D ** -0.5), new(F, D, scale=D ** -0.5), new(D, F, scale=F ** -0.5), new(M, D)]
+    held = [torch.zeros_like(t) for t in fresh]
+    w = new(d)
+    positions = torch.arange(M, device="cuda")[:, None]
+    plan = rl.Rope((d,), pairing=rl.ROPE_HALF)
+    side = torch.cuda.Stream()
+
+    def step():
+        for a, b in zip(held, fresh):  # inputs and weights written right before the calls that read them
+            a.copy_(b)
+        x, gate, up, down, dy = held
+        q = x.view(M, H, d)
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            turned, _ = rl.qk_norm_rope(q, None, w, None, positions, plan)
+            y2 = rl.gated_mlp(turned.view(M, D), gate, up, down, act=rl.ACT_GELU)
+        y, saved = rl.gated_mlp(x, gate, up, down, save=True)
+        here.wait_stream(side)
+        grads = rl.gated_mlp_backward(dy + y2, x, gate, up, down, saved)
+        back = rl.qk_norm_rope_backward(grads[0].view(M, H, d), None, q, None, w, None, positions, plan)
+        return (y, y2) + grads + (back[0], back[2])
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(3):
+        for t in fresh:
+            t.copy_(torch.randn(t.shape, device="cuda", generator=gen) * t.float().std())
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert rl.rtlynx_stream_status() == rl.OK
