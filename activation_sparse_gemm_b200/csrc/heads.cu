@@ -584,16 +584,22 @@ int lanes_of(int64_t dim) {
 }
 int heads_per_pass(int64_t dim) { return 32 / lanes_of(dim); }
 
-// How a tensor's token-heads are dealt to warps.  A group of lanes takes all
-// heads of its token, so that angles are computed once, unless that leaves
-// fewer than about 16 warps an SM: then the heads are cut into shorter runs.
-void deal(HeadTensor& t, int64_t rows, int64_t heads, int64_t dim, int num_sms, bool persistent) {
-    const int64_t per_pass = heads_per_pass(dim);
-    const int64_t slots = (rows + per_pass - 1) / per_pass;
-    const int64_t want = 16ll * num_sms;
+// Heads that a group of lanes takes of its token: all of them, so that angles
+// are computed once, unless that leaves too few warps for the GPU; then shorter
+// runs, for the tensor with more heads 16 warps an SM (backward, where 16 run at
+// once for both tensors, 8: 2048 tokens of 40 + 8 heads of 128 take 26 us, 28 with
+// 16).  The other tensor's runs are as long.
+int64_t run_length(int64_t rows, int64_t most_heads, int64_t dim, int num_sms, bool backward) {
+    const int64_t slots = (rows + heads_per_pass(dim) - 1) / heads_per_pass(dim);
+    const int64_t want = (backward ? 8ll : 16ll) * num_sms;
     int64_t groups = slots >= want ? 1 : (want + slots - 1) / slots;
-    if (groups > heads) groups = heads;
-    t.run = static_cast<uint32_t>((heads + groups - 1) / groups);
+    if (groups > most_heads) groups = most_heads;
+    return (most_heads + groups - 1) / groups;
+}
+
+void deal(HeadTensor& t, int64_t rows, int64_t heads, int64_t run, int64_t dim, int num_sms, bool backward) {
+    const int64_t slots = (rows + heads_per_pass(dim) - 1) / heads_per_pass(dim);
+    t.run = static_cast<uint32_t>(run < heads ? run : heads);
     t.groups = static_cast<uint32_t>((heads + t.run - 1) / t.run);
     t.heads = static_cast<uint32_t>(heads);
     t.rows = static_cast<uint32_t>(rows);
@@ -603,7 +609,7 @@ void deal(HeadTensor& t, int64_t rows, int64_t heads, int64_t dim, int num_sms, 
     // backward: one block an SM and tensor (both tensors' blocks run at once),
     // each with one row of partial sums
     int64_t most = 1ll << 30;
-    if (persistent) most = num_sms < kHeadGradRows ? num_sms : kHeadGradRows;
+    if (backward) most = num_sms < kHeadGradRows ? num_sms : kHeadGradRows;
     t.blocks = static_cast<uint32_t>(blocks < most ? blocks : most);
 }
 
@@ -737,6 +743,9 @@ int run_heads(int kind, float sin_sign, const Call& call, int64_t B, int64_t S, 
     const int rc = device_info(&num_sms, &err);
     if (rc) return rc;
 
+    const int64_t rows = B * S;
+    const int64_t most_heads = tensors == 2 && call.x[1]->heads > call.x[0]->heads ? call.x[1]->heads : call.x[0]->heads;
+    const int64_t run = run_length(rows, most_heads, D, num_sms, kind == kNormBackward);
     for (int t = 0; t < tensors; ++t) {
         HeadTensor& h = args.t[t];
         h.x = call.x[t]->ptr;
@@ -748,9 +757,8 @@ int run_heads(int kind, float sin_sign, const Call& call, int64_t B, int64_t S, 
             h.gb = call.dy[t]->stride_b, h.gs = call.dy[t]->stride_s, h.gh = call.dy[t]->stride_h;
         }
         h.w = call.w[t];
-        const int64_t rows = B * S;
         if (rows * call.x[t]->heads > (int64_t(1) << 31)) return RTLYNX_ERR_UNSUPPORTED;  // items fit 32 bits
-        deal(h, rows, call.x[t]->heads, D, num_sms, kind == kNormBackward);
+        deal(h, rows, call.x[t]->heads, run, D, num_sms, kind == kNormBackward);
         if (call.dw[t])
             h.part = static_cast<float*>(workspace) + static_cast<size_t>(t) * kHeadGradRows * D;
     }
