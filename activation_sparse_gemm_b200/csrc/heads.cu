@@ -23,7 +23,7 @@
 //
 // Measured (32760 tokens, 40 + 40 heads of 128, bf16, 1.34 GB): rotation 207 us
 // (6.5 TB/s, the measured copy rate), with the norm 220 us (6.1 TB/s); gradient
-// of both on 16384 tokens (1.01 GB) 169 us (6.0 TB/s).
+// of both on 16384 tokens (1.01 GB) 164 us (6.1 TB/s).
 //
 // Angles: position x frequency / 2 pi in 64 bits, reduced to an eighth of a
 // turn there, so a position of 2^24 loses nothing; sine and cosine of the
@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
     const HeadTensor& t = args.t[keys ? 1 : 0];
     const uint32_t block = blockIdx.x - (keys ? args.t[0].blocks : 0u);
 
-    // a head takes `lanes` lanes (some of them idle where they are LANES), a
-    // pass of the warp as many heads as fit
+    // a head takes `lanes` lanes (some of them idle where they are LANES), and
+    // the warp as many tokens as fit
     const int lanes = LANES > 0 ? LANES : args.dim / 8;
     const int per_pass = 32 / lanes;
     const int chunk = lane % lanes, sub = lane / lanes;
