@@ -21,10 +21,12 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.util
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "librtlynx.so")
+TORCH_LIB_PATH = os.path.join(_PKG, "_lib", "rtlynx_torch.so")
 
 MODE_SPARSE = 0
 MODE_DENSE_SKIP = 1
@@ -377,23 +379,37 @@ def linear(X, W, L_A=None, L_B=None, mode: int = MODE_SPARSE, out=None, stream=N
     return Y
 
 
+# The operators around the linear layers.  Checks, outputs and the call itself are compiled (csrc/torch_calls.cpp):
+# a call on a few tokens is as long as its host part.
+_calls = None
 _HERE = contextlib.nullcontext()
 
 
-def _launch_on(device, stream):
-    """(stream handle, context) of a torch-level call: the tensors' device, and the stream whose allocator pool the
-    call's outputs and workspace come from (`stream`, or the device's current one), so that memory is never handed on
-    while in use."""
+def _torch_calls():
+    global _calls
+    if _calls is None:
+        import torch  # noqa: F401  (the extension needs its libraries in the process)
+        if not os.path.exists(TORCH_LIB_PATH):
+            raise RuntimeError(f"{TORCH_LIB_PATH} is missing: build it with "
+                               "`python -m activation_sparse_gemm_b200.build`")
+        spec = importlib.util.spec_from_file_location("rtlynx_torch", TORCH_LIB_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        L = lib()
+        module.bind({name: ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in ABI_SYMBOLS})
+        _calls = module
+    return _calls
+
+
+def _on(tensor, stream):
+    """The context in which a call on `tensor` runs on `stream` (a torch stream or a handle): outputs and workspaces
+    then come from that stream's pool, so that memory is never handed on while in use."""
     import torch
-    index = device.index
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
-        return handle, (_HERE if torch.cuda.current_device() == index else torch.cuda.device(device))
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    elif stream.device != device:
-        raise ValueError(f"stream of {stream.device}, tensors on {device}")
-    return int(stream.cuda_stream), torch.cuda.stream(stream)
+        stream = torch.cuda.ExternalStream(stream, device=tensor.device)
+    elif stream.device != tensor.device:
+        raise ValueError(f"stream of {stream.device}, tensors on {tensor.device}")
+    return torch.cuda.stream(stream)
 
 
 class Rope:
@@ -426,135 +442,29 @@ class Rope:
         self._freq = (ctypes.c_double * pairs)(*values)
         dims = (ctypes.c_int32 * MAX_AXES)(*self.axes)
         freq = ctypes.cast(self._freq, ctypes.POINTER(ctypes.c_double))
-        self.specs = tuple(RopeSpec(len(self.axes), dims, int(pairing), t, 0.0, freq)
-                           for t in (POS_INT32, POS_INT64, POS_FP32))
-
-
-_dtype_codes, _pos_types = {}, {}
-
-
-def _codes(table, names):
-    """Fills a torch dtype -> ABI code table on first use (torch is imported late)."""
-    import torch
-    if not table:
-        table.update((getattr(torch, n), i) for i, n in enumerate(names))
-    return table
-
-
-def _heads_view(t, shape, dtype, device, what):
-    """HeadsView of t [S, H, D] or [B, S, H, D] (any strides, channels contiguous), checked against the first tensor's
-    dtype, device and shape (the heads aside, where shape has None)."""
-    st, sh = t.stride(), t.shape
-    n = len(sh)
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{what}: {t.dtype} on {t.device}, expected {dtype} on {device}")
-    if n != len(shape) or sh[-1] != shape[-1] or sh[0] != shape[0] or sh[-3] != shape[-3] or \
-            (shape[-2] is not None and sh[-2] != shape[-2]):
-        raise ValueError(f"{what}: shape {tuple(sh)}, expected {tuple(shape)}")
-    if st[-1] != 1 and sh[-1] > 1:
-        raise ValueError(f"{what}: the channels of a head are contiguous, got strides {st}")
-    return HeadsView(t.data_ptr(), sh[-2], st[0] if n == 4 else 0, st[-3], st[-2])
-
-
-class _HeadsCall:
-    """The checked arguments that every query/key call shares."""
-
-    __slots__ = ("shape", "kshape", "dtype", "device", "B", "S", "D", "code", "spec", "strides", "handle", "ctx")
-
-    def __init__(self, q, k, positions, rope, stream):
-        shape = q.shape
-        n = len(shape)
-        if n not in (3, 4) or not q.is_cuda:
-            raise ValueError(f"CUDA tensors [S, H, D] or [B, S, H, D], got {tuple(shape)} on {q.device}")
-        self.shape, self.dtype, self.device = shape, q.dtype, q.device
-        self.kshape = None if k is None else (*shape[:-2], None, shape[-1])
-        self.B, S, self.D = (shape[0] if n == 4 else 1), shape[-3], shape[-1]
-        self.S = S
-        self.code = (_dtype_codes or _codes(_dtype_codes, ("bfloat16", "float16", "float32"))).get(self.dtype)
-        if self.code is None:
-            raise ValueError(f"bf16, fp16 or fp32 tensors, got {self.dtype}")
-        # positions [S, axes], shared by the sequences, or [B, S, axes]
-        kind = (_pos_types or _codes(_pos_types, ("int32", "int64", "float32"))).get(positions.dtype)
-        if kind is None or positions.device != self.device:
-            raise ValueError(f"positions: int32, int64 or float32 on {self.device}, got {positions.dtype} on "
-                             f"{positions.device}")
-        at, axes = positions.shape, len(rope.axes)
-        if at == (S, axes):
-            self.strides = (0, *positions.stride())
-        elif at == (self.B, S, axes):
-            self.strides = positions.stride()
-        else:
-            raise ValueError(f"positions {tuple(at)}, expected {(S, axes)} or {(self.B, S, axes)}")
-        self.spec = rope.specs[kind]
-        self.handle, self.ctx = _launch_on(self.device, stream)
-
-    def first(self, t):
-        """View of the tensor that the others are checked against."""
-        st, sh = t.stride(), self.shape
-        if st[-1] != 1 and sh[-1] > 1:
-            raise ValueError(f"the channels of a head are contiguous, got strides {st}")
-        return HeadsView(t.data_ptr(), sh[-2], st[0] if len(sh) == 4 else 0, st[-3], st[-2])
-
-    def view(self, t, what, keys=False):
-        if t is None:
-            return None
-        return _heads_view(t, self.kshape if keys else self.shape, self.dtype, self.device, what)
-
-    def weight(self, w, what):
-        if w is None:
-            return None
-        if w.shape != (self.D,) or w.dtype != self.dtype or w.device != self.device or not w.is_contiguous():
-            raise ValueError(f"{what}: contiguous [{self.D}] {self.dtype} on {self.device}")
-        return w.data_ptr()
-
-    def outputs(self, out, q, k):
-        """((queries, view), (keys, view)) of `out`, or of new contiguous tensors."""
-        if out is not None:
-            return (out[0], self.view(out[0], "q_out")), \
-                (None, None) if k is None else (out[1], _heads_view(out[1], k.shape, self.dtype, self.device, "k_out"))
-        return self.new(q), (None, None) if k is None else self.new(k)
-
-    def new(self, like):
-        import torch
-        t = torch.empty_like(like, memory_format=torch.contiguous_format)
-        row = like.shape[-2] * self.D
-        return t, HeadsView(t.data_ptr(), like.shape[-2], self.S * row, row, self.D)
-
-
-def _run_rope(name, q, k, positions, rope, out, stream):
-    c = _HeadsCall(q, k, positions, rope, stream)
-    with c.ctx:
-        (qo, qo_view), (ko, ko_view) = c.outputs(out, q, k)
-        status = getattr(lib(), name)(c.first(q), c.view(k, "k", True), qo_view, ko_view, c.B, c.S, c.D, c.code,
-                                      c.spec, positions.data_ptr(), *c.strides, c.handle)
-    if status:
-        _check(status, name)
-    return qo, ko
+        self.specs = (RopeSpec * 3)(*(RopeSpec(len(self.axes), dims, int(pairing), t, 0.0, freq)
+                                      for t in (POS_INT32, POS_INT64, POS_FP32)))
+        self._at = ctypes.addressof(self.specs)
 
 
 def rope(q, k, positions, rope, out=None, stream=None):
     """(R q, R k) for q [B, S, Hq, D] and k [B, S, Hk, D] (or [S, H, D], or k None), any strides.
 
     positions [S, axes] or [B, S, axes] (int32, int64, float32), rope a Rope; out=(q, k) works in place."""
-    return _run_rope("rtlynx_rope", q, k, positions, rope, out, stream)
+    with _HERE if stream is None else _on(q, stream):
+        return _torch_calls().rope(False, q, k, positions, rope._at, len(rope.axes), out)
 
 
 def rope_backward(dq_out, dk_out, positions, rope, out=None, stream=None):
     """Gradients of rope()'s inputs from those of its outputs; out=(dq_out, dk_out) works in place."""
-    return _run_rope("rtlynx_rope_backward", dq_out, dk_out, positions, rope, out, stream)
+    with _HERE if stream is None else _on(dq_out, stream):
+        return _torch_calls().rope(True, dq_out, dk_out, positions, rope._at, len(rope.axes), out)
 
 
 def qk_norm_rope(q, k, w_q, w_k, positions, rope, eps=1e-6, out=None, stream=None):
     """rope() of the heads' RMS norms: (R (w_q q / rms q), R (w_k k / rms k)); w_q, w_k [D] in q's type, or None."""
-    c = _HeadsCall(q, k, positions, rope, stream)
-    with c.ctx:
-        (qo, qo_view), (ko, ko_view) = c.outputs(out, q, k)
-        status = lib().rtlynx_qk_norm_rope(c.first(q), c.view(k, "k", True), c.weight(w_q, "w_q"),
-                                           c.weight(w_k, "w_k"), qo_view, ko_view, c.B, c.S, c.D, c.code, eps, c.spec,
-                                           positions.data_ptr(), *c.strides, c.handle)
-    if status:
-        _check(status, "rtlynx_qk_norm_rope")
-    return qo, ko
+    with _HERE if stream is None else _on(q, stream):
+        return _torch_calls().qk_norm_rope(q, k, w_q, w_k, positions, rope._at, len(rope.axes), eps, out)
 
 
 def qk_norm_rope_backward(dq_out, dk_out, q, k, w_q, w_k, positions, rope, eps=1e-6, out=None, weight_grads=True,
@@ -562,45 +472,9 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, w_q, w_k, positions, rope, eps=1
     """(dq, dk, dw_q, dw_k) of qk_norm_rope(); dw_q, dw_k are float32 [D], None without weight_grads or a weight.
 
     out=(dq_out, dk_out) or out=(q, k) works in place."""
-    import torch
-    if (dk_out is None) != (k is None):
-        raise ValueError("dk_out goes with k")
-    c = _HeadsCall(q, k, positions, rope, stream)
-    with c.ctx:
-        (dq, dq_view), (dk, dk_view) = c.outputs(out, q, k)
-        dw_q = torch.empty(c.D, dtype=torch.float32, device=c.device) if weight_grads and w_q is not None else None
-        dw_k = torch.empty(c.D, dtype=torch.float32, device=c.device) \
-            if weight_grads and w_k is not None and k is not None else None
-        ws, ws_bytes = None, 0
-        if dw_q is not None or dw_k is not None:
-            ws_bytes = rtlynx_qk_norm_rope_workspace_size(c.D)
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=c.device)
-
-        gk_view = None if k is None else _heads_view(dk_out, k.shape, c.dtype, c.device, "dk_out")
-        status = lib().rtlynx_qk_norm_rope_backward(
-            c.view(dq_out, "dq_out"), gk_view, c.first(q), c.view(k, "k", True), c.weight(w_q, "w_q"),
-            c.weight(w_k, "w_k"), dq_view, dk_view, _ptr(dw_q), _ptr(dw_k), c.B, c.S, c.D, c.code, eps, c.spec,
-            positions.data_ptr(), *c.strides, _ptr(ws), ws_bytes, c.handle)
-    _check(status, "rtlynx_qk_norm_rope_backward")
-    return dq, dk, dw_q, dw_k
-
-
-def _matrix(t, rows, cols, device, what, dtype=None):
-    """The address of t, checked: a contiguous bf16 CUDA matrix of this shape on this device."""
-    import torch
-    dtype = dtype or torch.bfloat16
-    if t.dtype != dtype or t.device != device or t.shape != (rows, cols) or not t.is_contiguous():
-        raise ValueError(f"{what}: contiguous {dtype} {(rows, cols)} on {device}, got {t.dtype} {tuple(t.shape)} on "
-                         f"{t.device}")
-    return t.data_ptr()
-
-
-def _gated_inputs(X, W_gate, W_up, W_down):
-    if not X.is_cuda or X.dim() != 2 or W_gate.dim() != 2:
-        raise ValueError("X [M, D] and W_gate [D_ff, D] are CUDA matrices")
-    (M, D), F, device = X.shape, W_gate.shape[0], X.device
-    return (M, D, F), (_matrix(X, M, D, device, "X"), _matrix(W_gate, F, D, device, "W_gate"),
-                       _matrix(W_up, F, D, device, "W_up"), _matrix(W_down, D, F, device, "W_down"))
+    with _HERE if stream is None else _on(q, stream):
+        return _torch_calls().qk_norm_rope_backward(dq_out, dk_out, q, k, w_q, w_k, positions, rope._at,
+                                                    len(rope.axes), eps, out, weight_grads)
 
 
 def gated_mlp(X, W_gate, W_up, W_down, act=ACT_SILU, L_A=None, L_B=None, mode_down=MODE_DENSE_SKIP, save=False,
@@ -611,47 +485,13 @@ def gated_mlp(X, W_gate, W_up, W_down, act=ACT_SILU, L_A=None, L_B=None, mode_do
     With mode_down=MODE_SPARSE the down-projection is the activation-sparse layer with the LoRA pair L_A [D, R],
     L_B [R, D_ff].  With save=True the result is (Y, saved), saved = (G, U, low, H) for gated_mlp_backward
     (low: the bits of G and U below bf16's, as int16; see include/rtlynx.h)."""
-    import torch
-    (M, D, F), at = _gated_inputs(X, W_gate, W_up, W_down)
-    device = X.device
-    R = 0 if (L_A is None or L_B is None or mode_down == MODE_DENSE_SKIP) else L_B.shape[0]
-    la = _matrix(L_A, D, R, device, "L_A") if R else None
-    lb = _matrix(L_B, R, F, device, "L_B") if R else None
-    handle, ctx = _launch_on(device, stream)
-    with ctx:
-        if out is None:
-            Y = torch.empty_like(X)
-            y = Y.data_ptr()
-        else:
-            Y, y = out, _matrix(out, M, D, device, "out")
-        H = torch.empty((M, F), dtype=X.dtype, device=device)
-        G = U = low = None
-        if save:
-            G, U, low = torch.empty_like(H), torch.empty_like(H), torch.empty_like(H, dtype=torch.int16)
-        ws_bytes = lib().rtlynx_gated_mlp_block_workspace_size(M, D, F, mode_down)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
-        status = lib().rtlynx_gated_mlp_block(*at, la, lb, _ptr(G), _ptr(U), _ptr(low), H.data_ptr(), y, M, D, F,
-                                              R, act, mode_down, _ptr(ws), ws_bytes, handle)
-    _check(status, "rtlynx_gated_mlp_block")
-    return (Y, (G, U, low, H)) if save else Y
+    with _HERE if stream is None else _on(X, stream):
+        return _torch_calls().gated_mlp(X, W_gate, W_up, W_down, act, L_A, L_B, mode_down, save, out)
 
 
 def gated_mlp_backward(dY, X, W_gate, W_up, W_down, saved, act=ACT_SILU, needs=(True, True, True, True), stream=None):
     """(dX, dW_gate, dW_up, dW_down) of gated_mlp with a dense down-projection, from dY [M, D] and its `saved`.
 
     needs: which of the four to compute; the others are None."""
-    import torch
-    (M, D, F), at = _gated_inputs(X, W_gate, W_up, W_down)
-    device = X.device
-    dy = _matrix(dY, M, D, device, "dY")
-    kept = [_matrix(t, M, F, device, name, torch.int16 if name == "low" else None)
-            for t, name in zip(saved, ("G", "U", "low", "H"), strict=True)]
-    handle, ctx = _launch_on(device, stream)
-    with ctx:
-        grads = tuple(torch.empty_like(t) if need else None for t, need in zip((X, W_gate, W_up, W_down), needs, strict=True))
-        ws_bytes = rtlynx_gated_mlp_backward_workspace_size(M, D, F)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
-        status = lib().rtlynx_gated_mlp_backward(dy, *at, *kept, *(_ptr(g) for g in grads), M, D, F, act,
-                                                 ws.data_ptr(), ws_bytes, handle)
-    _check(status, "rtlynx_gated_mlp_backward")
-    return grads
+    with _HERE if stream is None else _on(X, stream):
+        return _torch_calls().gated_mlp_backward(dY, X, W_gate, W_up, W_down, saved, act, [bool(n) for n in needs])

@@ -1,4 +1,5 @@
-"""Builds the CUDA library librtlynx.so in-tree for sm_100a (nvcc, no GPU needed).
+"""Builds the CUDA library librtlynx.so in-tree for sm_100a (nvcc, no GPU needed),
+and rtlynx_torch.so, the host code of its torch-level calls.
 
     python -m activation_sparse_gemm_b200.build [--force] [--verbose-ptxas]
 """
@@ -6,16 +7,21 @@ from __future__ import annotations
 
 import argparse
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "librtlynx.so")
+TORCH_SRC = os.path.join(CSRC, "torch_calls.cpp")
+TORCH_LIB = os.path.join(LIB_DIR, "rtlynx_torch.so")
+HEADER = os.path.join(ROOT, "include", "rtlynx.h")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -24,6 +30,14 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def host_compiler() -> str:
+    """The system's g++: the extension has to share torch's libstdc++, which a toolchain of its own may link statically."""
+    for cand in ("/usr/bin/g++", shutil.which("g++")):
+        if cand and os.path.exists(cand):
+            return cand
+    raise RuntimeError("g++ not found")
 
 
 def sources():
@@ -39,7 +53,28 @@ def needs_build() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def build_torch_calls(force: bool = False) -> str:
+    """Compiles the torch-level calls against the installed torch (g++, about 20 s)."""
+    if not force and os.path.exists(TORCH_LIB) and \
+            os.path.getmtime(TORCH_LIB) >= max(os.path.getmtime(TORCH_SRC), os.path.getmtime(HEADER)):
+        return TORCH_LIB
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    os.makedirs(LIB_DIR, exist_ok=True)
+    tmp = TORCH_LIB + f".{os.getpid()}.tmp"
+    subprocess.check_call([
+        host_compiler(), "-O2", "-std=c++17", "-fPIC", "-shared",
+        "-DTORCH_EXTENSION_NAME=rtlynx_torch", "-I" + sysconfig.get_paths()["include"],
+        "-I" + os.path.join(torch_dir, "include"),
+        "-I" + os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+        "-I" + os.path.join(cuda, "include"), TORCH_SRC, "-o", tmp, "-L" + os.path.join(torch_dir, "lib"), "-lc10",
+        "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"])
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    build_torch_calls(force)
     if not force and not needs_build():
         return LIB
     os.makedirs(LIB_DIR, exist_ok=True)
