@@ -251,7 +251,7 @@ __device__ __forceinline__ void load_rows32(const uint16_t* base, int row0, int 
     for (int i = 0; i < 4; ++i) {
         const int row = row0 + (lane & ~3) + i, c = col + 8 * u;
         v[i] = make_uint4(0, 0, 0, 0);
-        if (row < rows && c < cols) v[i] = __ldg(reinterpret_cast<const uint4*>(base + static_cast<size_t>(row) * cols + c));
+        if (row < rows && c < cols) v[i] = *reinterpret_cast<const uint4*>(base + static_cast<size_t>(row) * cols + c);
     }
 }
 
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(256) rtlynx_gated_sum_parts_kernel(const __gri
     if constexpr (EPI == kStore) {
         write(0, pack8(f));
     } else {
-        auto read = [&](int i) { return __ldg(reinterpret_cast<const uint4*>(p.in[i] + at)); };
+        auto read = [&](int i) { return *reinterpret_cast<const uint4*>(p.in[i] + at); };
         float g[8], u[8];
         restore8(read(0), read(1), read(2), g, u);
 #pragma unroll

@@ -20,7 +20,8 @@
 // Measured at D = 5120, D_ff = 13824 (424.7 MB of weights, 64.9 us at the
 // measured copy rate): 1 token 70 us (6.0 TB/s), 8 tokens 74; 16 tokens 88, as a
 // block re-reads the tokens from L2 half as often as it reads weights, which is
-// where gated_some.cu takes over.  11 tokens at 2056 -> 5512: 19 us.
+// where gated_some.cu takes over.  11 tokens at 2056 -> 5512: 22 us (19 when the
+// weights are in L2).
 #include "../../include/rtlynx.h"
 #include "act.cuh"
 #include "internal.h"
@@ -38,11 +39,14 @@ struct FewArgs {
     int M, N, K;
 };
 
+// Not the read-only path: this kernel may have been launched while the one
+// that writes its weights was still running.
 __device__ __forceinline__ uint4 load_weights(const uint16_t* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+                 : "l"(p)
+                 : "memory");
     return v;
 }
 
