@@ -584,33 +584,50 @@ int lanes_of(int64_t dim) {
 }
 int heads_per_pass(int64_t dim) { return 32 / lanes_of(dim); }
 
+int64_t slots_of(int64_t rows, int64_t dim) { return (rows + heads_per_pass(dim) - 1) / heads_per_pass(dim); }
+
 // Heads that a group of lanes takes of its token: all of them, so that angles
-// are computed once, unless that leaves too few warps for the GPU; then shorter
-// runs, for the tensor with more heads 16 warps an SM (backward, where 16 run at
-// once for both tensors, 8: 2048 tokens of 40 + 8 heads of 128 take 26 us, 28 with
-// 16).  The other tensor's runs are as long.
-int64_t run_length(int64_t rows, int64_t most_heads, int64_t dim, int num_sms, bool backward) {
-    const int64_t slots = (rows + heads_per_pass(dim) - 1) / heads_per_pass(dim);
-    const int64_t want = (backward ? 8ll : 16ll) * num_sms;
+// are computed once, unless that leaves the tensor with more heads fewer than
+// `want` warps; then shorter runs, as long for the other tensor.
+int64_t run_length(int64_t rows, int64_t most_heads, int64_t dim, int64_t want) {
+    const int64_t slots = slots_of(rows, dim);
     int64_t groups = slots >= want ? 1 : (want + slots - 1) / slots;
     if (groups > most_heads) groups = most_heads;
     return (most_heads + groups - 1) / groups;
 }
 
-void deal(HeadTensor& t, int64_t rows, int64_t heads, int64_t run, int64_t dim, int num_sms, bool backward) {
-    const int64_t slots = (rows + heads_per_pass(dim) - 1) / heads_per_pass(dim);
+void deal(HeadTensor& t, int64_t rows, int64_t heads, int64_t run, int64_t dim, int64_t most_blocks) {
     t.run = static_cast<uint32_t>(run < heads ? run : heads);
     t.groups = static_cast<uint32_t>((heads + t.run - 1) / t.run);
     t.heads = static_cast<uint32_t>(heads);
     t.rows = static_cast<uint32_t>(rows);
-    const int64_t items = slots * t.groups;
+    const int64_t items = slots_of(rows, dim) * t.groups;
     t.items = static_cast<uint32_t>(items);
     const int64_t blocks = (items + kHeadWarps - 1) / kHeadWarps;
-    // backward: one block an SM and tensor (both tensors' blocks run at once),
-    // each with one row of partial sums
-    int64_t most = 1ll << 30;
-    if (backward) most = num_sms < kHeadGradRows ? num_sms : kHeadGradRows;
-    t.blocks = static_cast<uint32_t>(blocks < most ? blocks : most);
+    t.blocks = static_cast<uint32_t>(blocks < most_blocks ? blocks : most_blocks);
+}
+
+// Both tensors' work.  Forward, as many blocks as there are items for, 16 warps
+// an SM asked for.  Backward, where a block keeps a row of partial sums, the two
+// blocks an SM that run at once, shared out by the tensors' heads (three more
+// for a token's angles).
+void deal_all(HeadTensor (&t)[2], const int64_t (&heads)[2], int tensors, int64_t rows, int64_t dim, int num_sms,
+              bool backward) {
+    const int big = tensors == 2 && heads[1] > heads[0] ? 1 : 0;
+    int64_t blocks[2] = {int64_t(1) << 30, int64_t(1) << 30}, want = 16ll * num_sms;
+    if (backward) {
+        const int64_t all = 2 * num_sms < kHeadGradRows ? 2 * num_sms : kHeadGradRows;
+        blocks[big] = all;
+        if (tensors == 2) {
+            const int64_t mine = heads[big] + 3, other = heads[1 - big] + 3;
+            blocks[1 - big] = all * other / (mine + other);
+            if (blocks[1 - big] < 1) blocks[1 - big] = 1;
+            blocks[big] = all - blocks[1 - big];
+        }
+        want = blocks[big] * kHeadWarps;
+    }
+    const int64_t run = run_length(rows, heads[big], dim, want);
+    for (int i = 0; i < tensors; ++i) deal(t[i], rows, heads[i], run, dim, blocks[i]);
 }
 
 template <typename T, int LANES>
@@ -744,8 +761,7 @@ int run_heads(int kind, float sin_sign, const Call& call, int64_t B, int64_t S, 
     if (rc) return rc;
 
     const int64_t rows = B * S;
-    const int64_t most_heads = tensors == 2 && call.x[1]->heads > call.x[0]->heads ? call.x[1]->heads : call.x[0]->heads;
-    const int64_t run = run_length(rows, most_heads, D, num_sms, kind == kNormBackward);
+    int64_t heads[2] = {};
     for (int t = 0; t < tensors; ++t) {
         HeadTensor& h = args.t[t];
         h.x = call.x[t]->ptr;
@@ -758,10 +774,11 @@ int run_heads(int kind, float sin_sign, const Call& call, int64_t B, int64_t S, 
         }
         h.w = call.w[t];
         if (rows * call.x[t]->heads > (int64_t(1) << 31)) return RTLYNX_ERR_UNSUPPORTED;  // items fit 32 bits
-        deal(h, rows, call.x[t]->heads, run, D, num_sms, kind == kNormBackward);
+        heads[t] = call.x[t]->heads;
         if (call.dw[t])
             h.part = static_cast<float*>(workspace) + static_cast<size_t>(t) * kHeadGradRows * D;
     }
+    deal_all(args.t, heads, tensors, rows, D, num_sms, kind == kNormBackward);
     args.positions = positions;
     args.pb = pos_stride_b, args.ps = pos_stride_s, args.pa = pos_stride_a;
     args.pos_type = spec->pos_type;
