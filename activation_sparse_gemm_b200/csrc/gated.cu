@@ -801,13 +801,17 @@ int down_parts(int64_t M, int64_t D, int64_t F) { return most_parts(tiles_of(M, 
 // 5120 -> 13824: 73 us against 90; at 4096 -> 11008 53 and 70; but at 2048 -> 5632
 // 24.4 against 22.8).  Up to 128 tokens gated_some.cu's down-projection (64 at
 // 5120 -> 13824: 88 us against 97 for the call, 128 at 256 -> 512: 11.2 and 11.7;
-// at 256 tokens 115 and 113), and its gate and up projections where there are
+// at 256 tokens 115 and 113).  Its gate and up projections where there are
 // enough tiles of 128 channels for the SMs, and the more the more tokens: half
 // of 3 / 2 a token (64 at 5120 -> 13824: 77 us against 88, at 2048 -> 5632 27.9 and
-// 28.3, at 1024 -> 2816 18.4 against 16.4).
+// 28.3, at 1024 -> 2816 18.4 against 16.4); and where rows are short, so that the
+// epilogue is what counts (128 at 256 -> 512: 8.7 us against 9.2, at 512 -> 8192 19.9
+// and 21.1; at 2472 -> 864 25.8 against 21.4).
 bool few_kernels(int64_t M, int64_t D, int64_t F) { return M <= 8 || (M <= kFewTokens && 6 * D * F <= 128000000); }
 bool some_down(int64_t M) { return M <= kSomeTokens; }
-bool some_gate(int64_t M, int64_t F) { return M <= kSomeTokens && 2 * M <= 3 * ceil_div(F, 128); }
+bool some_gate(int64_t M, int64_t D, int64_t F) {
+    return M <= kSomeTokens && (2 * M <= 3 * ceil_div(F, 128) || D <= 512);
+}
 
 // dH = dY Wd, where that saves more than the extra kernel costs: at 95 tokens and
 // 2472 -> 864 its four tiles have 39 stages each (training step 50 us, 68 with the
@@ -929,7 +933,7 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
                    ? RTLYNX_ERR_CUDA
                    : RTLYNX_OK;
     }
-    if (some_gate(M, D_ff)) {
+    if (some_gate(M, D, D_ff)) {
         if (launch_gated_some(X, W_gate, W_up, H, G, U, low, M, D, D_ff, act, err, stream)) return RTLYNX_ERR_CUDA;
     } else {
         GatedArgs args{};

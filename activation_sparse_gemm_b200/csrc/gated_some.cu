@@ -11,13 +11,15 @@
 // lie in the same tensor-memory lanes, so the activation needs no exchange.
 //
 // Measured at 5120 -> 13824 (424.7 MB of weights, 64.9 us at the measured copy
-// rate): 17 tokens 73 us, 64 tokens 77, 128 tokens 86; with gated.cu's kernels 92,
+// rate): 17 tokens 73 us, 64 tokens 76, 128 tokens 82; with gated.cu's kernels 92,
 // 97 and 103.  From 128 tokens on the epilogue, which no other tile's main
 // loop hides, costs what the loads save.
 //
 // One output tile a CTA.  The second kernel's tiles are cut along K so that
 // every SM has a part; the parts are left in fp32 in the caller's workspace and
-// added in order.  It requests its first weights before the first kernel has
+// added in order.  Tiles that are neither cut nor enough for the SMs share their
+// tokens out over several CTAs (128 tokens at 256 -> 512: 8.7 us, 11.1 with all
+// tokens in one).  The second kernel requests its first weights before the first kernel has
 // finished.
 #include "../../include/rtlynx.h"
 #include "act.cuh"
@@ -27,7 +29,7 @@
 namespace rtlynx {
 namespace {
 
-constexpr int kSomeThreads = 320;               // loads, MMAs, eight warps of epilogue
+constexpr int kSomeThreads = 64 + 512;           // at most: loads, MMAs, sixteen warps of epilogue
 constexpr int kRows = 128;                       // weight rows of a tile
 constexpr int kWeightBytes = kRows * 64 * 2;     // of one weight, a stage
 constexpr int kMaxStages = 8;
@@ -40,7 +42,7 @@ struct SomeArgs {
     uint16_t* out[4];  // [tokens, rows]: H, G, U, low (the last three may be null, see gated.cu); or the one output
     float* part;       // [split][tokens, rows] where K is cut
     int tokens, rows;
-    int n;             // tokens of the MMA, a multiple of 16
+    int n;             // tokens of a CTA, a multiple of 16
     int k, split;      // stages of a row, parts they are cut into
     int ring, columns; // pipeline stages; tensor-memory columns
     int* err;
@@ -59,6 +61,7 @@ __global__ void __launch_bounds__(kSomeThreads, 1) rtlynx_gated_some_kernel(cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row0 = blockIdx.x * kRows;
     const int part = blockIdx.y;
+    const int token0 = blockIdx.z * args.n;
     const int kb = part * args.k / args.split, ke = (part + 1) * args.k / args.split;
     const uint32_t stage_bytes = static_cast<uint32_t>(kMats * kWeightBytes + args.n * 128);
     int* err = args.err;
@@ -91,7 +94,7 @@ __global__ void __launch_bounds__(kSomeThreads, 1) rtlynx_gated_some_kernel(cons
             if (GATED) tma_load_2d(dst + kWeightBytes, &args.w[1], &full[stage], kt * 64, row0);
         };
         auto tokens = [&](int stage, int kt) {
-            tma_load_2d(smem + stage * stage_bytes + kMats * kWeightBytes, &args.x, &full[stage], kt * 64, 0);
+            tma_load_2d(smem + stage * stage_bytes + kMats * kWeightBytes, &args.x, &full[stage], kt * 64, token0);
         };
         const int ahead = min(args.ring, ke - kb);
         if constexpr (GATED) {
@@ -167,18 +170,22 @@ __global__ void __launch_bounds__(kSomeThreads, 1) rtlynx_gated_some_kernel(cons
         if (lane == 0) ok = mbar_wait(done, 0, err) ? 1u : 0u;
         if (__shfl_sync(0xFFFFFFFFu, ok, 0) && !error_seen(err)) {
             tc_fence_after();
-            // sixteen tokens at a time, every other sixteen for each of the two
-            // warps of a quadrant; the warp's lanes are consecutive channels, so
-            // each token's store is 64 contiguous bytes
-            for (int t0 = 16 * ((warp - 2) >> 2); t0 < args.tokens; t0 += 32) {
+            // sixteen tokens at a time, shared out over the two or four warps of
+            // a quadrant; the warp's lanes are consecutive channels, so each
+            // token's store is 64 contiguous bytes
+            const int round = static_cast<int>(blockDim.x - 64) / 8;
+            const int tokens = min(args.n, args.tokens - token0);
+            const size_t first = static_cast<size_t>(token0) * args.rows + row;
+            float* const out_part = GATED ? nullptr : args.part + static_cast<size_t>(part) * args.tokens * args.rows;
+            for (int t0 = 16 * ((warp - 2) >> 2); t0 < tokens; t0 += round) {
+                size_t at = first + static_cast<size_t>(t0) * args.rows;
                 uint32_t g[16], u[16];
                 tmem_ld_32x32b_x16(acc + static_cast<uint32_t>(t0), g);
                 if (GATED) tmem_ld_32x32b_x16(acc + static_cast<uint32_t>(args.n + t0), u);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    if (t0 + j >= args.tokens || row >= args.rows) continue;
-                    const size_t at = static_cast<size_t>(t0 + j) * args.rows + row;
+                for (int j = 0; j < 16; ++j, at += args.rows) {
+                    if (t0 + j >= tokens || row >= args.rows) continue;
                     const float v = __uint_as_float(g[j]);
                     if constexpr (GATED) {
                         args.out[0][at] = __bfloat16_as_ushort(__float2bfloat16_rn(act_value<ACT>(v) * __uint_as_float(u[j])));
@@ -188,7 +195,7 @@ __global__ void __launch_bounds__(kSomeThreads, 1) rtlynx_gated_some_kernel(cons
                             args.out[3][at] = static_cast<uint16_t>((g[j] >> 8 & 0xFFu) | (u[j] & 0xFF00u));
                         }
                     } else if (args.split > 1) {
-                        args.part[static_cast<size_t>(part) * args.tokens * args.rows + at] = v;
+                        out_part[at] = v;
                     } else {
                         args.out[0][at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
                     }
@@ -232,7 +239,7 @@ __global__ void __launch_bounds__(256) rtlynx_gated_some_sum_kernel(const float*
 
 template <bool GATED, int ACT>
 int launch_some(SomeArgs& args, const void* x, const void* w0, const void* w1, int64_t tokens, int64_t rows, int64_t K,
-                int split, cudaStream_t stream) {
+                int split, int groups, cudaStream_t stream) {
     auto kernel = rtlynx_gated_some_kernel<GATED, ACT>;
     static std::atomic<uint64_t> smem_set{0};
     int e = allow_max_dynamic_smem(kernel, smem_set);
@@ -240,7 +247,8 @@ int launch_some(SomeArgs& args, const void* x, const void* w0, const void* w1, i
     constexpr int kMats = GATED ? 2 : 1;
     args.tokens = static_cast<int>(tokens);
     args.rows = static_cast<int>(rows);
-    args.n = static_cast<int>((tokens + 15) / 16 * 16);
+    const int64_t sixteens = (tokens + 15) / 16;
+    args.n = static_cast<int>((sixteens + groups - 1) / groups * 16);
     args.k = static_cast<int>((K + 63) / 64);
     args.split = split;
     const int stage = kMats * kWeightBytes + args.n * 128;
@@ -253,11 +261,23 @@ int launch_some(SomeArgs& args, const void* x, const void* w0, const void* w1, i
     if (!e && GATED) e = encode_tmap_uncached(&args.w[1], type, w1, K, rows, K * 2, 64, kRows, swizzle);
     if (!e) e = encode_tmap_uncached(&args.x, type, x, K, tokens, K * 2, 64, args.n, swizzle);
     if (e) return e;
-    const dim3 grid(static_cast<unsigned>((rows + kRows - 1) / kRows), split);
-    return launch_dependent(kernel, grid, dim3(kSomeThreads), kSomeSmem, stream, args);
+    const dim3 grid(static_cast<unsigned>((rows + kRows - 1) / kRows), split,
+                    static_cast<unsigned>((tokens + args.n - 1) / args.n));
+    // Eight epilogue warps, sixteen from 64 tokens on: 128 tokens at 512 -> 8192
+    // take 18.2 us, 20.2 with eight; 17 at 256 -> 512 8.1, 8.4 with sixteen.
+    const int threads = args.n >= 64 ? kSomeThreads : 64 + 256;
+    return launch_dependent(kernel, grid, dim3(threads), kSomeSmem, stream, args);
 }
 
 }  // namespace
+
+// How many CTAs share the tokens of one tile of rows: while there are SMs left,
+// so that the epilogue, which no other tile's main loop hides, is spread over
+// them.  No fewer than 32 tokens each, one round of the epilogue's eight warps.
+int token_groups(int64_t tokens, int64_t ctas) {
+    const int64_t most = (tokens + 31) / 32, fill = 148 / ctas;
+    return static_cast<int>(fill < 1 ? 1 : (fill < most ? fill : most));
+}
 
 int launch_gated_some(const void* X, const void* W_gate, const void* W_up, void* H, void* G, void* U, void* low, int64_t M,
                       int64_t D, int64_t D_ff, int act, int* err, cudaStream_t stream) {
@@ -267,8 +287,9 @@ int launch_gated_some(const void* X, const void* W_gate, const void* W_up, void*
     args.out[2] = static_cast<uint16_t*>(U);
     args.out[3] = static_cast<uint16_t*>(low);
     args.err = err;
-    return act == RTLYNX_ACT_SILU ? launch_some<true, RTLYNX_ACT_SILU>(args, X, W_gate, W_up, M, D_ff, D, 1, stream)
-                                  : launch_some<true, RTLYNX_ACT_GELU>(args, X, W_gate, W_up, M, D_ff, D, 1, stream);
+    const int groups = token_groups(M, (D_ff + kRows - 1) / kRows);
+    return act == RTLYNX_ACT_SILU ? launch_some<true, RTLYNX_ACT_SILU>(args, X, W_gate, W_up, M, D_ff, D, 1, groups, stream)
+                                  : launch_some<true, RTLYNX_ACT_GELU>(args, X, W_gate, W_up, M, D_ff, D, 1, groups, stream);
 }
 
 int down_some_parts(int64_t D, int64_t D_ff) {
@@ -285,7 +306,8 @@ int launch_down_some(const void* H, const void* W_down, void* Y, float* part, in
     args.part = part;
     args.err = err;
     const int split = down_some_parts(D, D_ff);
-    const int e = launch_some<false, 0>(args, H, W_down, nullptr, M, D, D_ff, split, stream);
+    const int e = launch_some<false, 0>(args, H, W_down, nullptr, M, D, D_ff, split,
+                                           split > 1 ? 1 : token_groups(M, (D + kRows - 1) / kRows), stream);
     if (e || split == 1) return e;
     const int64_t n = M * D;
     return launch_dependent(rtlynx_gated_some_sum_kernel, dim3(static_cast<unsigned>((n / 8 + 255) / 256)), dim3(256), 0,
