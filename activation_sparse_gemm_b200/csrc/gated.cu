@@ -799,18 +799,30 @@ int down_parts(int64_t M, int64_t D, int64_t F) { return most_parts(tiles_of(M, 
 // Which kernels run the forward call.  Up to 8 tokens those of gated_few.cu; up
 // to 16 too, but with weights past 128 MB those of gated_some.cu (16 tokens at
 // 5120 -> 13824: 73 us against 90; at 4096 -> 11008 53 and 70; but at 2048 -> 5632
-// 24.4 against 22.8).  Up to 128 tokens gated_some.cu's down-projection (64 at
-// 5120 -> 13824: 88 us against 97 for the call, 128 at 256 -> 512: 11.2 and 11.7;
-// at 256 tokens 115 and 113).  Its gate and up projections where there are
-// enough tiles of 128 channels for the SMs, and the more the more tokens: half
-// of 3 / 2 a token (64 at 5120 -> 13824: 77 us against 88, at 2048 -> 5632 27.9 and
-// 28.3, at 1024 -> 2816 18.4 against 16.4); and where rows are short, so that the
-// epilogue is what counts (128 at 256 -> 512: 8.7 us against 9.2, at 512 -> 8192 19.9
-// and 21.1; at 2472 -> 864 25.8 against 21.4).
+// 24.4 against 22.8).
 bool few_kernels(int64_t M, int64_t D, int64_t F) { return M <= 8 || (M <= kFewTokens && 6 * D * F <= 128000000); }
-bool some_down(int64_t M) { return M <= kSomeTokens; }
+
+// gated_some.cu's down-projection up to 512 tokens (384 at 512 -> 8192: 24.3 us
+// for the call, 30.3 with the tiled one; at 4096 -> 1024 26.5 and 32.0; 256 at
+// 5120 -> 13824, the worst case, 110 and 108), with small weights up to 1024 (768
+// at 1024 -> 2816 23.9 and 29.0; 1024 at 5120 -> 13824 354 and 339).
+bool some_down(int64_t M, int64_t D, int64_t F) { return M <= 512 || (M <= 1024 && D * F <= 12000000); }
+
+// gated_some.cu's gate and up projections
+// - where there are enough tiles of 128 channels for the SMs, and the more the
+//   more tokens: half of 3 / 2 a token (64 at 5120 -> 13824: 77 us against 88, at
+//   2048 -> 5632 27.9 and 28.3, at 1024 -> 2816 18.4 against 16.4);
+// - where rows are short, so that the epilogue is what counts, and one round of
+//   tiles does (128 at 256 -> 512: 8.7 us against 9.2, at 512 -> 8192 18.3 and 21.1;
+//   at 2472 -> 864 25.8 against 21.4);
+// - where the tiled kernel would need a second round of tiles and this one does
+//   not, with 208 tokens a tile at most (384 at 2048 -> 5632: 36.1 us against 40.5,
+//   160 at 5120 -> 13824 88 and 97; 256 there 114 against 110).
 bool some_gate(int64_t M, int64_t D, int64_t F) {
-    return M <= kSomeTokens && (2 * M <= 3 * ceil_div(F, 128) || D <= 512);
+    const int64_t tiles = ceil_div(F, 128), sms = 2 * kPlanPairs;
+    if (M <= 256 && 2 * M <= 3 * tiles) return true;
+    if (D <= 512) return M <= 128 || (M <= 384 && tiles * ceil_div(M, 256) <= sms);
+    return M <= 512 && ceil_div(M, kTile) * tiles > kPlanPairs && tiles * ceil_div(M, 208) <= sms;
 }
 
 // dH = dY Wd, where that saves more than the extra kernel costs: at 95 tokens and
@@ -884,8 +896,8 @@ extern "C" {
 size_t rtlynx_gated_mlp_block_workspace_size(int64_t M, int64_t D, int64_t D_ff, int mode_down) {
     if (check_sizes(M, D, D_ff, RTLYNX_ACT_SILU) || few_kernels(M, D, D_ff)) return 0;
     if (mode_down != RTLYNX_MODE_DENSE_SKIP) return 0;
-    if (some_down(M)) {
-        const int split = down_some_parts(D, D_ff);
+    if (some_down(M, D, D_ff)) {
+        const int split = down_some_parts(M, D, D_ff);
         return split > 1 ? align256(static_cast<size_t>(split) * M * D * sizeof(float)) : 0;
     }
     const int split = down_parts(M, D, D_ff);
@@ -979,7 +991,7 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
     }
     if (mode_down == RTLYNX_MODE_SPARSE)
         return rtlynx_linear(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down, stream_);
-    if (some_down(M))
+    if (some_down(M, D, D_ff))
         return launch_down_some(H, W_down, Y, static_cast<float*>(workspace), M, D_ff, D, err, stream) ? RTLYNX_ERR_CUDA
                                                                                                        : RTLYNX_OK;
     GatedArgs args{};

@@ -4,23 +4,23 @@
 // The weights' bytes still bound it, so they take the MMA's long side: a CTA
 // computes D[128 weight rows, tokens], the weights are the A operand (128 rows
 // of 64 K values a stage, of both Wg and Wu in the first kernel), the tokens
-// its B (N = tokens rounded up to 16).  Nearly all of shared memory holds
-// weights on their way, 32 KB a stage for 64 tokens' 8 KB, which is what keeps
-// HBM busy: a CTA pair of gated.cu has 128 KB in flight of which it can use
+// its B (N = tokens rounded up to 16, 256 at most).  Nearly all of shared memory
+// holds weights on their way, 32 KB a stage for 64 tokens' 8 KB, which is what
+// keeps HBM busy: a CTA pair of gated.cu has 128 KB in flight of which it can use
 // half, here every SM has up to 160 KB.  Wg's and Wu's products for the same rows
 // lie in the same tensor-memory lanes, so the activation needs no exchange.
 //
 // Measured at 5120 -> 13824 (424.7 MB of weights, 64.9 us at the measured copy
-// rate): 17 tokens 73 us, 64 tokens 76, 128 tokens 82; with gated.cu's kernels 92,
-// 97 and 103.  From 128 tokens on the epilogue, which no other tile's main
-// loop hides, costs what the loads save.
+// rate): 17 tokens 73 us, 64 tokens 76, 128 tokens 82, 200 tokens 99; with
+// gated.cu's kernels 92, 97, 103 and 105.  At 2048 -> 5632: 129 tokens 29.6 us, 384
+// 36.1; with gated.cu's kernels 37.4 and 45.9.
 //
 // One output tile a CTA.  The second kernel's tiles are cut along K so that
 // every SM has a part; the parts are left in fp32 in the caller's workspace and
-// added in order.  Tiles that are neither cut nor enough for the SMs share their
-// tokens out over several CTAs (128 tokens at 256 -> 512: 8.7 us, 11.1 with all
-// tokens in one).  The second kernel requests its first weights before the first kernel has
-// finished.
+// added in order.  Where SMs are left, several CTAs share a tile's tokens (128
+// tokens at 256 -> 512: 8.7 us, 11.1 with all tokens in one; 256 at 384 -> 1024
+// 11.0 and 14.2).  The second kernel requests its first weights before the first
+// kernel has finished.
 #include "../../include/rtlynx.h"
 #include "act.cuh"
 #include "internal.h"
@@ -237,6 +237,16 @@ __global__ void __launch_bounds__(256) rtlynx_gated_some_sum_kernel(const float*
                                                      pack_bf16x2(sum[4], sum[5]), pack_bf16x2(sum[6], sum[7]));
 }
 
+// How many CTAs share the tokens of one tile of rows: while there are SMs left,
+// so that the epilogue, which no other tile's main loop hides, is spread over
+// them.  No fewer than 32 tokens each, one round of the epilogue's eight warps,
+// and no more than the MMA takes.
+int64_t least_groups(int64_t tokens) { return (tokens + 255) / 256; }
+int token_groups(int64_t tokens, int64_t tiles) {
+    const int64_t least = least_groups(tokens), most = (tokens + 31) / 32, fill = 148 / tiles;
+    return static_cast<int>(fill < least ? least : (fill < most ? fill : most));
+}
+
 template <bool GATED, int ACT>
 int launch_some(SomeArgs& args, const void* x, const void* w0, const void* w1, int64_t tokens, int64_t rows, int64_t K,
                 int split, int groups, cudaStream_t stream) {
@@ -271,14 +281,6 @@ int launch_some(SomeArgs& args, const void* x, const void* w0, const void* w1, i
 
 }  // namespace
 
-// How many CTAs share the tokens of one tile of rows: while there are SMs left,
-// so that the epilogue, which no other tile's main loop hides, is spread over
-// them.  No fewer than 32 tokens each, one round of the epilogue's eight warps.
-int token_groups(int64_t tokens, int64_t ctas) {
-    const int64_t most = (tokens + 31) / 32, fill = 148 / ctas;
-    return static_cast<int>(fill < 1 ? 1 : (fill < most ? fill : most));
-}
-
 int launch_gated_some(const void* X, const void* W_gate, const void* W_up, void* H, void* G, void* U, void* low, int64_t M,
                       int64_t D, int64_t D_ff, int act, int* err, cudaStream_t stream) {
     SomeArgs args{};
@@ -292,10 +294,14 @@ int launch_gated_some(const void* X, const void* W_gate, const void* W_up, void*
                                   : launch_some<true, RTLYNX_ACT_GELU>(args, X, W_gate, W_up, M, D_ff, D, 1, groups, stream);
 }
 
-int down_some_parts(int64_t D, int64_t D_ff) {
-    const int64_t tiles = (D + kRows - 1) / kRows, stages = (D_ff + 63) / 64;
-    int64_t split = 148 / tiles;
-    if (split > stages / 8) split = stages / 8;
+int down_some_parts(int64_t M, int64_t D, int64_t D_ff) {
+    const int64_t ctas = (D + kRows - 1) / kRows * least_groups(M), stages = (D_ff + 63) / 64;
+    // parts of eight stages at least; past 128 tokens, where adding the parts
+    // takes longer, of twelve (384 tokens at 512 -> 8192: 24.3 us, 26.1 with eight;
+    // 64 at 512 -> 1536 12.0, 12.5 with twelve)
+    const int64_t least = M <= 128 ? 8 : 12;
+    int64_t split = 148 / ctas;
+    if (split > stages / least) split = stages / least;
     return static_cast<int>(split < 1 ? 1 : (split > 16 ? 16 : split));
 }
 
@@ -305,9 +311,9 @@ int launch_down_some(const void* H, const void* W_down, void* Y, float* part, in
     args.out[0] = static_cast<uint16_t*>(Y);
     args.part = part;
     args.err = err;
-    const int split = down_some_parts(D, D_ff);
+    const int split = down_some_parts(M, D, D_ff);
     const int e = launch_some<false, 0>(args, H, W_down, nullptr, M, D, D_ff, split,
-                                           split > 1 ? 1 : token_groups(M, (D + kRows - 1) / kRows), stream);
+                                           token_groups(M, (D + kRows - 1) / kRows * split), stream);
     if (e || split == 1) return e;
     const int64_t n = M * D;
     return launch_dependent(rtlynx_gated_some_sum_kernel, dim3(static_cast<unsigned>((n / 8 + 255) / 256)), dim3(256), 0,

@@ -175,12 +175,11 @@ int launch_gated_few(const void* X, const void* W_gate, const void* W_up, void* 
                      int D, int D_ff, int act, cudaStream_t stream);
 int launch_down_few(const void* H, const void* W_down, void* Y, int M, int D_ff, int D, cudaStream_t stream);
 
-// The same for up to kSomeTokens tokens (gated_some.cu); the down-projection's
-// parts are [down_some_parts][M, D] floats.
-constexpr int kSomeTokens = 128;
+// The same for some hundred tokens (gated_some.cu); the down-projection's parts
+// are [down_some_parts][M, D] floats.
 int launch_gated_some(const void* X, const void* W_gate, const void* W_up, void* H, void* G, void* U, void* low, int64_t M,
                       int64_t D, int64_t D_ff, int act, int* err, cudaStream_t stream);
-int down_some_parts(int64_t D, int64_t D_ff);
+int down_some_parts(int64_t M, int64_t D, int64_t D_ff);
 int launch_down_some(const void* H, const void* W_down, void* Y, float* part, int64_t M, int64_t D_ff, int64_t D, int* err,
                      cudaStream_t stream);
 

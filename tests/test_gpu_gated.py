@@ -26,7 +26,8 @@ H_STEP = 2.0 ** -8
 SIZES = [(1, 8, 8), (1, 64, 136), (2, 1032, 264), (3, 72, 40), (5, 520, 1000), (8, 136, 264), (9, 2056, 552),
          (16, 256, 128), (17, 136, 264), (33, 264, 72), (64, 64, 64), (128, 256, 512), (129, 200, 328), (256, 512, 256),
          (257, 520, 136), (300, 1032, 520), (700, 264, 1160), (1025, 72, 2056), (40, 264, 4104), (520, 136, 6152), (2900, 136, 72),
-         (30, 2056, 264), (270, 2312, 520), (24, 136, 2312), (65, 200, 6152), (128, 72, 11016), (10, 4104, 5512)]
+         (30, 2056, 264), (270, 2312, 520), (24, 136, 2312), (65, 200, 6152), (128, 72, 11016), (10, 4104, 5512),
+         (200, 72, 11016), (130, 520, 11144), (380, 520, 4872), (500, 520, 4872), (1024, 264, 1544), (384, 264, 136)]
 
 
 def ints(gen, shape, low, high, density):
