@@ -82,6 +82,7 @@ struct Problem {
     int rows, cols;             // of the output
     int out[4];                 // maps of the outputs; forward: H, G, U, low (the last three may be -1); backward: dG, dU
     uint16_t* sum_out[2];       // split > 1: the outputs themselves, for the summing kernel
+    int sum_pitch;              // values from one of their rows to the next
     const uint16_t* in[3];      // backward: G, U, low
     float* part;                // split > 1: fp32 partial tiles
 };
@@ -654,7 +655,8 @@ __global__ void __launch_bounds__(256) rtlynx_gated_sum_parts_kernel(const __gri
     const int col = nt * kTile + 8 * octet;
     if (row >= p.rows || col >= p.cols) return;
     const size_t at = static_cast<size_t>(row) * p.cols + col;
-    auto write = [&](int i, uint4 v) { *reinterpret_cast<uint4*>(p.sum_out[i] + at) = v; };
+    const size_t to = static_cast<size_t>(row) * p.sum_pitch + col;
+    auto write = [&](int i, uint4 v) { *reinterpret_cast<uint4*>(p.sum_out[i] + to) = v; };
     float f[8];
     sum_octet(p, tile, rank, row_in_cta, octet, f);
     if constexpr (EPI == kStore) {
@@ -716,21 +718,26 @@ struct Maps {
     GatedArgs& args;
     int count = 0;
     bool ok = true;
-    // a [rows, cols] bf16 matrix read in boxes of 64 contiguous values x box_rows
-    int add(const void* base, int64_t rows, int64_t cols, bool mn, int box_rows = kHalf) {
-        if (encode_tmap_uncached(&args.maps[count], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, cols * 2, 64,
+    // a bf16 matrix [rows, cols], its rows `pitch` values apart, read in boxes
+    // of 64 contiguous values x box_rows
+    int add_pitched(const void* base, int64_t rows, int64_t cols, int64_t pitch, bool mn, int box_rows = kHalf) {
+        if (encode_tmap_uncached(&args.maps[count], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, pitch * 2, 64,
                                  mn ? 64 : box_rows, CU_TENSOR_MAP_SWIZZLE_128B))
             ok = false;
         return count++;
     }
-    // a [rows, cols] bf16 output, written in 32 x 32 pieces
-    int out(void* base, int64_t rows, int64_t cols) {
+    int add(const void* base, int64_t rows, int64_t cols, bool mn, int box_rows = kHalf) {
+        return add_pitched(base, rows, cols, cols, mn, box_rows);
+    }
+    // a bf16 output, written in 32 x 32 pieces
+    int out_pitched(void* base, int64_t rows, int64_t cols, int64_t pitch) {
         if (!base) return -1;
-        if (encode_tmap_uncached(&args.maps[count], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, cols * 2, 32, 32,
+        if (encode_tmap_uncached(&args.maps[count], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, pitch * 2, 32, 32,
                                  CU_TENSOR_MAP_SWIZZLE_64B))
             ok = false;
         return count++;
     }
+    int out(void* base, int64_t rows, int64_t cols) { return out_pitched(base, rows, cols, cols); }
 };
 
 int check_sizes(int64_t M, int64_t D, int64_t F, int act) {
@@ -868,11 +875,16 @@ struct BackwardLayout {
     size_t dg, du, part, total;
 };
 
+// Values from one row of dG and dU to the next: they live in the workspace, so
+// their rows start on 128-byte lines whatever D_ff (2047 tokens at 1544 -> 4104:
+// training step 277 us with rows of D_ff values, 258 like this).
+int64_t hidden_pitch(int64_t F) { return (F + 63) / 64 * 64; }
+
 // The workspace does for any choice of gradients.
 BackwardLayout backward_layout(int64_t M, int64_t D, int64_t F) {
     BackwardLayout l;
     l.dg = 0;
-    l.du = align256(static_cast<size_t>(M) * F * 2);
+    l.du = align256(static_cast<size_t>(M) * hidden_pitch(F) * 2);
     l.part = 2 * l.du;
     int64_t units = 0;
     const int dh = dh_parts(M, D, F);
@@ -1008,6 +1020,7 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
     p.b0 = p.b1 = maps.add(W_down, D, D_ff, false);
     p.out[0] = maps.out(Y, M, D);
     p.sum_out[0] = static_cast<uint16_t*>(Y);
+    p.sum_pitch = static_cast<int>(D);
     if (!maps.ok) return RTLYNX_ERR_CUDA;
     p.group_n = raster_group(p, pairs);
     p.rows = static_cast<int>(M);
@@ -1046,6 +1059,7 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
     uint16_t* dG = reinterpret_cast<uint16_t*>(base + l.dg);
     uint16_t* dU = reinterpret_cast<uint16_t*>(base + l.du);
 
+    const int64_t h_pitch = hidden_pitch(D_ff);
     const int m_pairs = ceil_div(M, kTile), token_stages = ceil_div(M, 64);
     if (dX || dW_gate || dW_up) {
         // dH = dY Wd, taken to dG and dU before it leaves the chip
@@ -1062,10 +1076,11 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         p.a0 = p.a1 = maps.add(dY, M, D, false);
         p.b0 = p.b1 = maps.add(W_down, D, D_ff, true);
         p.b_mn = 1;
-        p.out[0] = maps.out(dG, M, D_ff);
-        p.out[1] = maps.out(dU, M, D_ff);
+        p.out[0] = maps.out_pitched(dG, M, D_ff, h_pitch);
+        p.out[1] = maps.out_pitched(dU, M, D_ff, h_pitch);
         p.sum_out[0] = dG;
         p.sum_out[1] = dU;
+        p.sum_pitch = static_cast<int>(h_pitch);
         if (!maps.ok) return RTLYNX_ERR_CUDA;
         p.group_n = raster_group(p, num_sms / 2);
         p.rows = static_cast<int>(M);
@@ -1090,6 +1105,7 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         p.cols = static_cast<int>(cols);
         p.out[0] = maps.out(out, rows, cols);
         p.sum_out[0] = static_cast<uint16_t*>(out);
+        p.sum_pitch = static_cast<int>(cols);
         p.group_n = raster_group(p, pairs);
         p.first_unit = args.units;
         args.units += p.m_pairs * p.n_tiles * p.split;
@@ -1108,28 +1124,28 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         Problem& p = args.p[args.problems];
         p.k0 = ceil_div(D_ff, 64);
         p.k = 2 * p.k0;
-        p.a0 = maps.add(dG, M, D_ff, false);
+        p.a0 = maps.add_pitched(dG, M, D_ff, h_pitch, false);
         p.b0 = maps.add(W_gate, D_ff, D, true);
-        p.a1 = maps.add(dU, M, D_ff, false);
+        p.a1 = maps.add_pitched(dU, M, D_ff, h_pitch, false);
         p.b1 = maps.add(W_up, D_ff, D, true);
         p.b_mn = 1;
         parts_of(p, plan.x_tiles, plan.x_split);
         close(p, M, D, dX);
     };
-    auto weight_grad = [&](const void* a, int64_t a_cols, const void* b, int64_t b_cols, void* out) {
+    auto weight_grad = [&](const void* a, int64_t a_cols, int64_t a_pitch, const void* b, int64_t b_cols, void* out) {
         if (!out) return;
         Problem& p = args.p[args.problems];
         p.k0 = p.k = token_stages;
-        p.a0 = p.a1 = maps.add(a, M, a_cols, true);
+        p.a0 = p.a1 = maps.add_pitched(a, M, a_cols, a_pitch, true);
         p.b0 = p.b1 = maps.add(b, M, b_cols, true);
         p.a_mn = p.b_mn = 1;
         parts_of(p, plan.w_tiles, plan.w_split);
         close(p, a_cols, b_cols, out);
     };
     auto add_weights = [&]() {
-        weight_grad(dG, D_ff, X, D, dW_gate);
-        weight_grad(dU, D_ff, X, D, dW_up);
-        weight_grad(dY, D, H, D_ff, dW_down);
+        weight_grad(dG, D_ff, h_pitch, X, D, dW_gate);
+        weight_grad(dU, D_ff, h_pitch, X, D, dW_up);
+        weight_grad(dY, D, D, H, D_ff, dW_down);
     };
     // The longer units first; see Units for what the pairs with one of them
     // less take instead.
