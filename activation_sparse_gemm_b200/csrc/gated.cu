@@ -172,13 +172,14 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
         : "memory");
 }
 
-// 128 x 64 values into shared memory, 128B swizzle.  K-major: 128 rows of 64
-// K values.  MN-major: two boxes of 64 row values x 64 K.
-template <bool MN>
+// 128 x 64 values into shared memory (64 x 64 of B of a narrow tile), 128B
+// swizzle.  K-major: rows of 64 K values, as many as the map's box has.
+// MN-major: boxes of 64 row values x 64 K.
+template <bool MN, int ROWS = kHalf>
 __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, uint32_t bar, int k, int row) {
     if (MN) {
         tma_load_pair(dst, map, bar, row, k);
-        tma_load_pair(dst + kOperandBytes / 2, map, bar, row + 64, k);
+        if (ROWS > 64) tma_load_pair(dst + kOperandBytes / 2, map, bar, row + 64, k);
     } else {
         tma_load_pair(dst, map, bar, k, row);
     }
@@ -283,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr int kColumns = TN / 2;  // rows of B a CTA holds
     constexpr int kStageBytes = kOperandBytes + kColumns * 64 * 2;
     constexpr int kStages = kStagingBytes / kStageBytes;
-    static_assert(EPI == kGatedForward || TN == kTile, "only the forward epilogue has narrow tiles");
+    static_assert(EPI != kStore || TN == kTile, "narrow tiles are for one-product launches with an epilogue of their own");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* pieces = smem + kStagingBytes;
@@ -352,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (elect_one()) {
                     if (leader) mbar_arrive_expect_tx(&full[stage], 2u * kStageBytes);
                     load_operand<A_MN>(dst, ma, bar, k, row0);
-                    load_operand<B_MN>(dst + kOperandBytes, mb, bar, k, col0);
+                    load_operand<B_MN, kColumns>(dst + kOperandBytes, mb, bar, k, col0);
                 }
                 if (++stage == kStages) {
                     stage = 0;
@@ -363,7 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; ok && units.at(i, args, w); ++i) {
             const Problem& p = args.p[w.problem];
             const int row0 = w.mp * kTile + static_cast<int>(rank) * kHalf;
-            const int col0 = EPI == kGatedForward ? w.nt * kColumns : w.nt * kTile + static_cast<int>(rank) * kHalf;
+            const int col0 = EPI == kGatedForward ? w.nt * kColumns : w.nt * TN + static_cast<int>(rank) * kColumns;
             // one run of stages for each operand pair
             for (int seg = 0; seg < 2 && ok; ++seg) {
                 const int begin = seg ? max(w.kb, p.k0) : w.kb, end = seg ? w.ke : min(w.ke, p.k0);
@@ -538,13 +539,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             } else if constexpr (EPI == kGatedBackward) {
-                constexpr int kCols = kTile / (kEpiWarps / 4);
+                constexpr int kCols = TN / (kEpiWarps / 4);
                 const int c0 = part * kCols;
 #pragma unroll 1
                 for (int c = c0; c < c0 + kCols; c += 32) {
                     uint32_t r[32];
                     uint4 gp[4], up[4], lp[4];
-                    const int col0 = w.nt * kTile + c;
+                    const int col0 = w.nt * TN + c;
                     if (row0 >= p.rows || col0 >= p.cols) break;  // the same in the whole warp
                     load_rows32(p.in[0], row0, col0, p.rows, p.cols, gp);
                     load_rows32(p.in[1], row0, col0, p.rows, p.cols, up);
@@ -832,6 +833,16 @@ bool some_gate(int64_t M, int64_t D, int64_t F) {
     return M <= 512 && ceil_div(M, kTile) * tiles > kPlanPairs && tiles * ceil_div(M, 208) <= sms;
 }
 
+// Narrow tiles where rounds of them over the pairs end sooner than rounds of
+// wide ones, twice as long each: with 200 tokens, 13824 columns of H are 108
+// tiles for 74 pairs (two rounds) or 216 (three of half the length).
+// 128 tokens at 256 -> 512: 12.3 us, 14.1 wide; 64 at 5120 -> 13824 92.6 and 96.7
+// (before they had kernels of their own).  Past four rounds wide tiles win by
+// reading X half as often (900 at 2048 -> 8192: 81 us, 88 narrow).
+bool narrow_tiles(int64_t rows, int64_t wide, int64_t thin, int64_t pairs) {
+    return rows * thin <= 4 * pairs && ceil_div(rows * thin, pairs) < 2 * ceil_div(rows * wide, pairs);
+}
+
 // dH = dY Wd, where that saves more than the extra kernel costs: at 95 tokens and
 // 2472 -> 864 its four tiles have 39 stages each (training step 50 us, 68 with the
 // tiles whole).  The gate and up projections are not cut: it made 957 tokens at
@@ -966,16 +977,7 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
         args.err = err;
         Problem& p = args.p[0];
         p.m_pairs = ceil_div(M, kTile);
-        // Tiles of 64 output columns where rounds of them over the pairs end
-        // sooner than rounds of 128: with 200 tokens, 13824 columns are 108
-        // tiles for 74 pairs (two rounds) or 216 (three of half the length).
-        // 128 tokens at 256 -> 512: 12.3 us, 14.1 wide; 64 at 5120 -> 13824 (before
-        // they had kernels of their own) 92.6 and 96.7.  Past four rounds wide
-        // tiles win by reading X half as often (900 at 2048 -> 8192: 81 us, 88
-        // narrow).
-        const int64_t wide = static_cast<int64_t>(p.m_pairs) * ceil_div(D_ff, kHalf);
-        const int64_t thin = static_cast<int64_t>(p.m_pairs) * ceil_div(D_ff, kNarrow / 2);
-        const bool narrow = thin <= 4ll * pairs && ceil_div(thin, pairs) < 2 * ceil_div(wide, pairs);
+        const bool narrow = narrow_tiles(p.m_pairs, ceil_div(D_ff, kHalf), ceil_div(D_ff, kNarrow / 2), pairs);
         const int columns = narrow ? kNarrow / 2 : kHalf;
         p.n_tiles = ceil_div(D_ff, columns);
         p.split = 1;
@@ -1069,8 +1071,10 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         args.err = err;
         Problem& p = args.p[0];
         p.m_pairs = m_pairs;
-        p.n_tiles = ceil_div(D_ff, kTile);
         p.split = dh_parts(M, D, D_ff);
+        // narrow tiles by the forward call's rule
+        const bool narrow = p.split == 1 && narrow_tiles(m_pairs, ceil_div(D_ff, kTile), ceil_div(D_ff, kNarrow), num_sms / 2);
+        p.n_tiles = ceil_div(D_ff, narrow ? kNarrow : kTile);
         p.part = reinterpret_cast<float*>(base + l.part);
         p.k0 = p.k = ceil_div(D, 64);
         p.a0 = p.a1 = maps.add(dY, M, D, false);
@@ -1089,8 +1093,13 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
         p.in[1] = static_cast<const uint16_t*>(U);
         p.in[2] = static_cast<const uint16_t*>(low);
         args.units = p.m_pairs * p.n_tiles * p.split;
-        const int e = act == RTLYNX_ACT_SILU ? launch_gated<kGatedBackward, RTLYNX_ACT_SILU>(args, num_sms, stream)
-                                             : launch_gated<kGatedBackward, RTLYNX_ACT_GELU>(args, num_sms, stream);
+        int e;
+        if (act == RTLYNX_ACT_SILU)
+            e = narrow ? launch_gated<kGatedBackward, RTLYNX_ACT_SILU, kNarrow>(args, num_sms, stream)
+                       : launch_gated<kGatedBackward, RTLYNX_ACT_SILU>(args, num_sms, stream);
+        else
+            e = narrow ? launch_gated<kGatedBackward, RTLYNX_ACT_GELU, kNarrow>(args, num_sms, stream)
+                       : launch_gated<kGatedBackward, RTLYNX_ACT_GELU>(args, num_sms, stream);
         if (e) return RTLYNX_ERR_CUDA;
     }
 
