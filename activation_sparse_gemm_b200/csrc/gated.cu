@@ -804,11 +804,21 @@ int most_parts(int64_t tiles, int64_t stages) {
 // parts of four.)
 int down_parts(int64_t M, int64_t D, int64_t F) { return most_parts(tiles_of(M, D), ceil_div(F, 64)); }
 
-// Which kernels run the forward call.  Up to 8 tokens those of gated_few.cu; up
-// to 16 too, but with weights past 128 MB those of gated_some.cu (16 tokens at
-// 5120 -> 13824: 73 us against 90; at 4096 -> 11008 53 and 70; but at 2048 -> 5632
-// 24.4 against 22.8).
-bool few_kernels(int64_t M, int64_t D, int64_t F) { return M <= 8 || (M <= kFewTokens && 6 * D * F <= 128000000); }
+// Which kernels run the forward call.  gated_few.cu's
+// - up to 8 tokens;
+// - up to 16, but with weights past 128 MB those of gated_some.cu (16 tokens at
+//   5120 -> 13824: 73 us against 90; at 4096 -> 11008 53 and 70; but at 2048 -> 5632
+//   24.4 against 22.8);
+// - up to 128 where weights and products are small (128 at 256 -> 512: 5.0 us
+//   against 8.9, at 1024 -> 1024 13.1 and 14.0; 48 at 1024 -> 2816 14.3 and 16.4; but
+//   17 at 1536 -> 4096 24 against 19), in about four blocks an SM at most (17 at
+//   512 -> 8192 in 1024 blocks 20 us against 15).
+bool few_kernels(int64_t M, int64_t D, int64_t F) {
+    if (M <= 8) return true;
+    if (M <= 16) return 6 * D * F <= 128000000;
+    const int64_t groups = (M + 15) / 16;
+    return M <= kFewTokens && 16 * groups * D * F <= 140000000 && groups * ceil_div(F, 16) <= 600;
+}
 
 // gated_some.cu's down-projection up to 512 tokens (384 at 512 -> 8192: 24.3 us
 // for the call, 30.3 with the tiled one; at 4096 -> 1024 26.5 and 32.0; 256 at

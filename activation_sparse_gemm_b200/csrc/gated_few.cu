@@ -17,11 +17,14 @@
 //
 // The warps' fp32 sums meet in shared memory and are added in warp order.
 //
+// Small weights stay in L2, and then more tokens do as well: blocks of 16 tokens
+// each, side by side, reading the same weights (64 tokens at 256 -> 512: 4.9 us,
+// 8.9 with gated_some.cu's kernels; 32 at 2472 -> 864 9.7 and 18.0).
+//
 // Measured at D = 5120, D_ff = 13824 (424.7 MB of weights, 64.9 us at the
-// measured copy rate): 1 token 70 us (6.0 TB/s), 8 tokens 74; 16 tokens 88, as a
+// measured copy rate): 1 token 67 us (6.4 TB/s), 8 tokens 69; 16 tokens 88, as a
 // block re-reads the tokens from L2 half as often as it reads weights, which is
-// where gated_some.cu takes over.  11 tokens at 2056 -> 5512: 22 us (19 when the
-// weights are in L2).
+// where gated_some.cu takes over.  11 tokens at 2056 -> 5512: 21 us.
 #include "../../include/rtlynx.h"
 #include "act.cuh"
 #include "internal.h"
@@ -60,9 +63,10 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 }
 
 // GATED: two matrices, act(first) * second; otherwise the one product.
-// TILES: tokens in eights.  WARPS: warps of a block.
-template <bool GATED, int TILES, int ACT, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) rtlynx_gated_few_kernel(const FewArgs args) {
+// TILES: a block's tokens in eights.  WARPS: warps of a block.  BLOCKS: resident on
+// an SM, which settles the registers of a thread.
+template <bool GATED, int TILES, int ACT, int WARPS, int BLOCKS>
+__global__ void __launch_bounds__(32 * WARPS, BLOCKS) rtlynx_gated_few_kernel(const FewArgs args) {
     constexpr int kFewWarps = WARPS, kFewThreads = 32 * WARPS;
     constexpr int kMats = GATED ? 2 : 1;
     constexpr int kUnroll = GATED ? 2 : 4;
@@ -72,6 +76,8 @@ __global__ void __launch_bounds__(32 * WARPS) rtlynx_gated_few_kernel(const FewA
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int row0 = blockIdx.x * kFewRows + g;
+    const int token0 = blockIdx.y * 8 * TILES, tokens = args.M - token0;
+    const uint16_t* const x0 = args.x + static_cast<size_t>(token0) * args.K;
     const bool row_ok[2] = {row0 < args.N, row0 + 8 < args.N};
     const size_t row_at[2] = {static_cast<size_t>(row0) * args.K, static_cast<size_t>(row0 + 8) * args.K};
     const int chunks = (args.K + 31) / 32;
@@ -120,8 +126,8 @@ __global__ void __launch_bounds__(32 * WARPS) rtlynx_gated_few_kernel(const FewA
             for (int n = 0; n < TILES; ++n) {
                 const int token = 8 * n + g;
                 x[u][n] = make_uint4(0, 0, 0, 0);
-                if (token < args.M && k < args.K)
-                    x[u][n] = *reinterpret_cast<const uint4*>(args.x + static_cast<size_t>(token) * args.K + k);
+                if (token < tokens && k < args.K)
+                    x[u][n] = *reinterpret_cast<const uint4*>(x0 + static_cast<size_t>(token) * args.K + k);
             }
         }
 #pragma unroll
@@ -150,7 +156,7 @@ __global__ void __launch_bounds__(32 * WARPS) rtlynx_gated_few_kernel(const FewA
         const int n = token / 8, col = token % 8;
         const int from = (ch % 8) * 4 + col / 2, j = (ch / 8) * 2 + col % 2;
         const int row = blockIdx.x * kFewRows + ch;
-        if (token >= args.M || row >= args.N) continue;
+        if (token >= tokens || row >= args.N) continue;
         float total[kMats];
 #pragma unroll
         for (int m = 0; m < kMats; ++m) {
@@ -158,7 +164,7 @@ __global__ void __launch_bounds__(32 * WARPS) rtlynx_gated_few_kernel(const FewA
 #pragma unroll
             for (int k = 0; k < kFewWarps; ++k) total[m] += sums[k][(m * TILES + n) * 4 + j][from];
         }
-        const size_t at = static_cast<size_t>(token) * args.N + row;
+        const size_t at = static_cast<size_t>(token0 + token) * args.N + row;
         if constexpr (GATED) {
             args.out[0][at] = __bfloat16_as_ushort(__float2bfloat16_rn(act_value<ACT>(total[0]) * total[1]));
             if (args.out[1]) {
@@ -173,24 +179,32 @@ __global__ void __launch_bounds__(32 * WARPS) rtlynx_gated_few_kernel(const FewA
     }
 }
 
-template <bool GATED, int ACT, int WARPS>
-int launch_warps(const FewArgs& args, cudaStream_t stream) {
-    const dim3 grid((args.N + kFewRows - 1) / kFewRows), block(32 * WARPS);
-    if (args.M <= 8) return launch_dependent(rtlynx_gated_few_kernel<GATED, 1, ACT, WARPS>, grid, block, 0, stream, args);
-    return launch_dependent(rtlynx_gated_few_kernel<GATED, 2, ACT, WARPS>, grid, block, 0, stream, args);
+template <bool GATED, int ACT, int WARPS, int BLOCKS>
+int launch_warps(const FewArgs& args, const dim3& grid, cudaStream_t stream) {
+    const dim3 block(32 * WARPS);
+    if (args.M <= 8)
+        return launch_dependent(rtlynx_gated_few_kernel<GATED, 1, ACT, WARPS, WARPS == 8 ? 3 : 1>, grid, block, 0, stream, args);
+    return launch_dependent(rtlynx_gated_few_kernel<GATED, 2, ACT, WARPS, BLOCKS>, grid, block, 0, stream, args);
 }
 
 template <bool GATED, int ACT>
 int launch_few(const FewArgs& args, cudaStream_t stream) {
+    int num_sms = 0;
+    int* err = nullptr;
+    if (device_info(&num_sms, &err)) return static_cast<int>(cudaErrorInvalidDevice);
+    const dim3 grid((args.N + kFewRows - 1) / kFewRows, (args.M + 15) / 16);
+    const int blocks = static_cast<int>(grid.x * grid.y);
     // Sixteen warps where there are no more blocks than SMs, so that enough
     // loads are in flight: at 2056 -> 5512 and 11 tokens the call takes 19.3 us,
     // 25.1 with eight.  With more blocks eight are as good or better (70 against
     // 77 us at 5120 -> 13824, one token).
-    int num_sms = 0;
-    int* err = nullptr;
-    if (device_info(&num_sms, &err)) return static_cast<int>(cudaErrorInvalidDevice);
-    const int blocks = (args.N + kFewRows - 1) / kFewRows;
-    return blocks <= num_sms ? launch_warps<GATED, ACT, 16>(args, stream) : launch_warps<GATED, ACT, 8>(args, stream);
+    if (blocks <= num_sms) return launch_warps<GATED, ACT, 16, 1>(args, grid, stream);
+    // Past eight tokens two blocks of 128 registers a thread on an SM, three of
+    // 80 where they are all resident then (11 tokens at 1536 -> 4096: 12.0 us,
+    // 13.6 with three; at 2056 -> 5512 22.1 and 21.2).  Up to eight tokens three
+    // (one at 5120 -> 13824: 66.6 us, 75.4 with two).
+    if (blocks > 2 * num_sms && blocks <= 3 * num_sms) return launch_warps<GATED, ACT, 8, 3>(args, grid, stream);
+    return launch_warps<GATED, ACT, 8, 2>(args, grid, stream);
 }
 
 }  // namespace

@@ -168,9 +168,9 @@ bool small_path_fits(const Dims& d, int num_sms);
 int launch_small(const Dims& d, const void* X, const void* W, const void* L_A, const void* L_B,
                  const Workspace& ws, void* Y, int* err, cudaStream_t stream);
 
-// The gated feed-forward block for at most kFewTokens tokens (gated_few.cu):
+// The gated feed-forward block for a few tokens, at most kFewTokens (gated_few.cu):
 // H (and G, U, low unless null) from X; Y = H W_down^T.
-constexpr int kFewTokens = 16;
+constexpr int kFewTokens = 128;
 int launch_gated_few(const void* X, const void* W_gate, const void* W_up, void* H, void* G, void* U, void* low, int M,
                      int D, int D_ff, int act, cudaStream_t stream);
 int launch_down_few(const void* H, const void* W_down, void* Y, int M, int D_ff, int D, cudaStream_t stream);
