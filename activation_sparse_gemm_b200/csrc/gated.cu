@@ -829,9 +829,9 @@ bool some_down(int64_t M, int64_t D, int64_t F) { return M <= 512 || (M <= 1024 
 // gated_some.cu's gate and up projections
 // - where there are enough tiles of 128 channels for the SMs, and the more the
 //   more tokens: half of 3 / 2 a token (64 at 5120 -> 13824: 77 us against 88, at
-//   2048 -> 5632 27.9 and 28.3, at 1024 -> 2816 18.4 against 16.4);
+//   2048 -> 5632 27.9 and 28.3, but 18.4 against 16.4 at 1024 -> 2816);
 // - where rows are short, so that the epilogue is what counts, and one round of
-//   tiles does (128 at 256 -> 512: 8.7 us against 9.2, at 512 -> 8192 18.3 and 21.1;
+//   tiles does (128 at 512 -> 8192: 18.3 us against 21.1, 200 there 22.1 and 22.5;
 //   at 2472 -> 864 25.8 against 21.4);
 // - where the tiled kernel would need a second round of tiles and this one does
 //   not, with 208 tokens a tile at most (384 at 2048 -> 5632: 36.1 us against 40.5,
@@ -846,8 +846,8 @@ bool some_gate(int64_t M, int64_t D, int64_t F) {
 // Narrow tiles where rounds of them over the pairs end sooner than rounds of
 // wide ones, twice as long each: with 200 tokens, 13824 columns of H are 108
 // tiles for 74 pairs (two rounds) or 216 (three of half the length).
-// 128 tokens at 256 -> 512: 12.3 us, 14.1 wide; 64 at 5120 -> 13824 92.6 and 96.7
-// (before they had kernels of their own).  Past four rounds wide tiles win by
+// 64 tokens at 5120 -> 13824: 92.6 us, 96.7 wide (before they had kernels of their
+// own).  Past four rounds wide tiles win by
 // reading X half as often (900 at 2048 -> 8192: 81 us, 88 narrow).
 bool narrow_tiles(int64_t rows, int64_t wide, int64_t thin, int64_t pairs) {
     return rows * thin <= 4 * pairs && ceil_div(rows * thin, pairs) < 2 * ceil_div(rows * wide, pairs);

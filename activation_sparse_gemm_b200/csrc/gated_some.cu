@@ -17,9 +17,8 @@
 //
 // One output tile a CTA.  The second kernel's tiles are cut along K so that
 // every SM has a part; the parts are left in fp32 in the caller's workspace and
-// added in order.  Where SMs are left, several CTAs share a tile's tokens (128
-// tokens at 256 -> 512: 8.7 us, 11.1 with all tokens in one; 256 at 384 -> 1024
-// 11.0 and 14.2).  The second kernel requests its first weights before the first
+// added in order.  Where SMs are left, several CTAs share a tile's tokens (256
+// tokens at 384 -> 1024: 11.0 us, 14.2 with all tokens in one).  The second kernel requests its first weights before the first
 // kernel has finished.
 #include "../../include/rtlynx.h"
 #include "act.cuh"
@@ -274,7 +273,7 @@ int launch_some(SomeArgs& args, const void* x, const void* w0, const void* w1, i
     const dim3 grid(static_cast<unsigned>((rows + kRows - 1) / kRows), split,
                     static_cast<unsigned>((tokens + args.n - 1) / args.n));
     // Eight epilogue warps, sixteen from 64 tokens on: 128 tokens at 512 -> 8192
-    // take 18.2 us, 20.2 with eight; 17 at 256 -> 512 8.1, 8.4 with sixteen.
+    // take 18.2 us, 20.2 with eight; 17 at 2048 -> 5632 24.9, 26.0 with sixteen.
     const int threads = args.n >= 64 ? kSomeThreads : 64 + 256;
     return launch_dependent(kernel, grid, dim3(threads), kSomeSmem, stream, args);
 }
@@ -296,12 +295,10 @@ int launch_gated_some(const void* X, const void* W_gate, const void* W_up, void*
 
 int down_some_parts(int64_t M, int64_t D, int64_t D_ff) {
     const int64_t ctas = (D + kRows - 1) / kRows * least_groups(M), stages = (D_ff + 63) / 64;
-    // parts of eight stages at least; past 128 tokens, where adding the parts
-    // takes longer, of twelve (384 tokens at 512 -> 8192: 24.3 us, 26.1 with eight;
-    // 64 at 512 -> 1536 12.0, 12.5 with twelve)
-    const int64_t least = M <= 128 ? 8 : 12;
+    // parts of twelve stages at least (384 tokens at 512 -> 8192: 24.3 us, 26.1 with
+    // eight, 24.6 with sixteen; 64 at 2048 -> 5632 25.1, 26.4 and 25.7)
     int64_t split = 148 / ctas;
-    if (split > stages / least) split = stages / least;
+    if (split > stages / 12) split = stages / 12;
     return static_cast<int>(split < 1 ? 1 : (split > 16 ? 16 : split));
 }
 
