@@ -18,8 +18,8 @@
 // One output tile a CTA.  The second kernel's tiles are cut along K so that
 // every SM has a part; the parts are left in fp32 in the caller's workspace and
 // added in order.  Where SMs are left, several CTAs share a tile's tokens (256
-// tokens at 384 -> 1024: 11.0 us, 14.2 with all tokens in one).  The second kernel requests its first weights before the first
-// kernel has finished.
+// tokens at 384 -> 1024: 11.0 us, 14.2 with all tokens in one).  The second kernel
+// requests its first weights before the first kernel has finished.
 #include "../../include/rtlynx.h"
 #include "act.cuh"
 #include "internal.h"
@@ -310,7 +310,7 @@ int launch_down_some(const void* H, const void* W_down, void* Y, float* part, in
     args.err = err;
     const int split = down_some_parts(M, D, D_ff);
     const int e = launch_some<false, 0>(args, H, W_down, nullptr, M, D, D_ff, split,
-                                           token_groups(M, (D + kRows - 1) / kRows * split), stream);
+                                        token_groups(M, (D + kRows - 1) / kRows * split), stream);
     if (e || split == 1) return e;
     const int64_t n = M * D;
     return launch_dependent(rtlynx_gated_some_sum_kernel, dim3(static_cast<unsigned>((n / 8 + 255) / 256)), dim3(256), 0,
