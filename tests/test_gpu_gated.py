@@ -253,7 +253,8 @@ def test_sparse_down_projection(act, M, D):
         assert torch.equal(y, rl.linear(H, W[2], la, lb, mode=rl.MODE_SPARSE))
 
 
-@pytest.mark.parametrize("M,D,F", [(1, 264, 520), (9, 264, 520), (140, 264, 520), (140, 2056, 4104)])
+@pytest.mark.parametrize("M,D,F", [(1, 264, 520), (9, 264, 520), (70, 264, 520), (140, 264, 520), (140, 2056, 4104),
+                                   (300, 1032, 2056)])
 def test_other_stream_and_captured_graph(M, D, F):
     gen = torch.Generator(device="cuda").manual_seed(3)
     def new(*shape):
