@@ -406,7 +406,9 @@ def _on(tensor, stream):
     then come from that stream's pool, so that memory is never handed on while in use."""
     import torch
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=tensor.device)
+        # handle 0, the default stream, is to torch a request for a stream of its pool
+        stream = (torch.cuda.ExternalStream(stream, device=tensor.device) if stream
+                  else torch.cuda.default_stream(tensor.device))
     elif stream.device != tensor.device:
         raise ValueError(f"stream of {stream.device}, tensors on {tensor.device}")
     return torch.cuda.stream(stream)
