@@ -948,11 +948,13 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
         return RTLYNX_ERR_INVALID_ARG;
     rc = validate(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down);
     if (rc) return rc;
-    const size_t need = rtlynx_gated_mlp_block_workspace_size(M, D, D_ff, mode_down);
+    const bool sparse = mode_down == RTLYNX_MODE_SPARSE;
+    const size_t need = sparse ? rtlynx_workspace_size(M, D_ff, D, R, mode_down)
+                               : rtlynx_gated_mlp_block_workspace_size(M, D, D_ff, mode_down);
     if (need > 0 && (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
         return RTLYNX_ERR_INVALID_ARG;
     const uint64_t x_bytes = 2ull * M * D, h_bytes = 2ull * M * D_ff, w_bytes = 2ull * D * D_ff;
-    const bool lora = mode_down == RTLYNX_MODE_SPARSE && R > 0;
+    const bool lora = sparse && R > 0;
     const Range in[6] = {{X, x_bytes},
                          {W_gate, w_bytes},
                          {W_up, w_bytes},
@@ -972,8 +974,9 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
         if (launch_gated_few(X, W_gate, W_up, H, G, U, low, static_cast<int>(M), static_cast<int>(D),
                              static_cast<int>(D_ff), act, stream))
             return RTLYNX_ERR_CUDA;
-        if (mode_down == RTLYNX_MODE_SPARSE)
-            return rtlynx_linear(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down, stream_);
+        if (sparse)
+            return rtlynx_linear_ws(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down, workspace, ws_bytes,
+                                    stream_);
         return launch_down_few(H, W_down, Y, static_cast<int>(M), static_cast<int>(D_ff), static_cast<int>(D), stream)
                    ? RTLYNX_ERR_CUDA
                    : RTLYNX_OK;
@@ -1013,8 +1016,8 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
                        : launch_gated<kGatedForward, RTLYNX_ACT_GELU>(args, num_sms, stream);
         if (e) return RTLYNX_ERR_CUDA;
     }
-    if (mode_down == RTLYNX_MODE_SPARSE)
-        return rtlynx_linear(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down, stream_);
+    if (sparse)
+        return rtlynx_linear_ws(H, W_down, LA_down, LB_down, Y, M, D_ff, D, R, mode_down, workspace, ws_bytes, stream_);
     if (some_down(M, D, D_ff))
         return launch_down_some(H, W_down, Y, static_cast<float*>(workspace), M, D_ff, D, err, stream) ? RTLYNX_ERR_CUDA
                                                                                                        : RTLYNX_OK;

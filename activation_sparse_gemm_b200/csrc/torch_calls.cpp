@@ -27,6 +27,7 @@ struct {
     decltype(&rtlynx_qk_norm_rope) norm_rope;
     decltype(&rtlynx_qk_norm_rope_backward) norm_rope_backward;
     decltype(&rtlynx_qk_norm_rope_workspace_size) norm_rope_workspace;
+    decltype(&rtlynx_workspace_size) linear_workspace;
     decltype(&rtlynx_gated_mlp_block) gated;
     decltype(&rtlynx_gated_mlp_block_workspace_size) gated_workspace;
     decltype(&rtlynx_gated_mlp_backward) gated_backward;
@@ -44,6 +45,7 @@ void bind(const py::dict& a) {
     take(api.norm_rope, a, "rtlynx_qk_norm_rope");
     take(api.norm_rope_backward, a, "rtlynx_qk_norm_rope_backward");
     take(api.norm_rope_workspace, a, "rtlynx_qk_norm_rope_workspace_size");
+    take(api.linear_workspace, a, "rtlynx_workspace_size");
     take(api.gated, a, "rtlynx_gated_mlp_block");
     take(api.gated_workspace, a, "rtlynx_gated_mlp_block_workspace_size");
     take(api.gated_backward, a, "rtlynx_gated_mlp_backward");
@@ -270,7 +272,8 @@ py::object gated_mlp(const Tensor& X, const Tensor& W_gate, const Tensor& W_up, 
         U = at::empty({g.M, g.F}, X.options());
         low = at::empty({g.M, g.F}, X.options().dtype(at::kShort));
     }
-    const size_t n = api.gated_workspace(g.M, g.D, g.F, mode_down);
+    const size_t n = mode_down == RTLYNX_MODE_SPARSE ? api.linear_workspace(g.M, g.F, g.D, R, mode_down)
+                                                     : api.gated_workspace(g.M, g.D, g.F, mode_down);
     if (n) ws = bytes(n, X);
     check(api.gated(g.x, g.gate, g.up, g.down, la, lb, data(G), data(U), data(low), H.data_ptr(), y, g.M, g.D, g.F, R, act,
                     mode_down, data(ws), n, c10::cuda::getCurrentCUDAStream(X.get_device()).stream()),

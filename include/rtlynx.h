@@ -211,10 +211,13 @@ int rtlynx_mlp_block(const void* X, const void* W_up, const void* LA_up, const v
  *      upper 16 (read as bf16: the projections, cut off), low the next eight of
  *      G in its low byte and of U in its high one; all three NULL where no
  *      gradient follows
- *   workspace: rtlynx_gated_mlp_block_workspace_size(M, D, D_ff, mode_down)
- *      bytes of device memory, 256-byte aligned, for this call until it has
- *      finished; the size may be 0 (always for invalid sizes, and for a sparse
- *      down layer, which uses the cached workspace of rtlynx_linear)
+ *   workspace: device memory, 256-byte aligned, for this call until it has
+ *      finished.  For a dense down layer
+ *      rtlynx_gated_mlp_block_workspace_size(M, D, D_ff, mode_down) bytes, which
+ *      may be 0 (and is for invalid sizes and for a sparse one).  For a sparse
+ *      down layer, whose need depends on its rank too,
+ *      rtlynx_workspace_size(M, D_ff, D, R, mode_down) bytes, what that layer
+ *      takes; the cached workspace of rtlynx_linear is not used
  * The projections are accumulated in 32 bits; H is made from them before they
  * are rounded.  Outputs may not share a byte with an input or one another.
  * M > 2^28, D or D_ff > 2^22 give RTLYNX_ERR_UNSUPPORTED.

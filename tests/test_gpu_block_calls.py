@@ -30,3 +30,45 @@ def test_handle_zero_is_the_default_stream():
     with torch.cuda.stream(side):  # the handle given, not the current stream, is where the call runs
         got = rl.gated_mlp(*args, stream=handle)
     assert torch.equal(got, want)
+
+
+SPARSE = [(1, 264, 520), (12, 264, 520), (200, 264, 520), (40, 2056, 520), (700, 264, 1032), (300, 1032, 2056)]
+
+
+def sparse_call(M, D, F, R=16, seed=0):
+    gen = torch.Generator(device="cuda").manual_seed(100 + seed)
+    args = gated_inputs(M, D, F, seed)
+    pair = dict(L_A=normal(gen, D, R, scale=0.1), L_B=normal(gen, R, F, scale=0.1)) if R else {}
+    return args, lambda **more: rl.gated_mlp(*args, mode_down=rl.MODE_SPARSE, **pair, **more)
+
+
+@pytest.mark.parametrize("R", [0, 16])
+@pytest.mark.parametrize("M,D,F", SPARSE)
+def test_sparse_down_in_captured_graphs(M, D, F, R):
+    """Captured on a stream that has made no call before, two graphs hold a workspace each: replayed at once on two
+    streams, behind larger eager calls on the stream of the capture, both give the eager result."""
+    (X, *_), call = sparse_call(M, D, F, R)
+    call()
+    _, larger = sparse_call(4 * M + 3, D + 8, F + 136, seed=1)
+    torch.cuda.synchronize()
+    capture = torch.cuda.Stream()
+    graphs, outs = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=capture):
+            outs.append(call())
+        graphs.append(graph)
+    for seed in range(2):
+        with torch.cuda.stream(capture):
+            X.copy_(normal(torch.Generator(device="cuda").manual_seed(seed), M, D))
+            want = call()
+            larger()
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in graphs]
+        for _ in range(4):
+            for graph, stream in zip(graphs, streams):
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, want) for out in outs)
+    assert rl.rtlynx_stream_status() == rl.OK
