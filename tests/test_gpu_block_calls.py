@@ -1,4 +1,6 @@
 """Calls of the query/key and gated operators as programs make them: handles of streams, several host threads."""
+import threading
+
 import pytest
 import torch
 
@@ -72,3 +74,41 @@ def test_sparse_down_in_captured_graphs(M, D, F, R):
         torch.cuda.synchronize()
         assert all(torch.equal(out, want) for out in outs)
     assert rl.rtlynx_stream_status() == rl.OK
+
+
+def in_threads(works):
+    """Runs the functions in a host thread each, at once; what they returned."""
+    results = [None] * len(works)
+
+    def run(i):
+        try:
+            results[i] = works[i]()
+        except Exception as e:  # reported by the caller's comparison
+            results[i] = e
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(works))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return results
+
+
+@pytest.mark.parametrize("M,D,F", [(128, 256, 256), (300, 264, 520), (12, 264, 520), (200, 264, 520), (700, 264, 1032)])
+def test_first_call_of_a_host_thread(M, D, F):
+    """A call that is all the CUDA work its thread has done, with nothing left to set up but the thread itself."""
+    X, gate, up, down = gated_inputs(M, D, F)
+    q = X[:, :256].unflatten(1, (2, 128))
+    positions, plan = torch.arange(M, device="cuda")[:, None], rl.Rope((128,))
+    _, saved = rl.gated_mlp(X, gate, up, down, save=True)
+    calls = [lambda: rl.linear(X, gate), lambda: rl.linear(X, gate, mode=rl.MODE_DENSE_SKIP),
+             lambda: rl.gated_mlp(X, gate, up, down),
+             lambda: rl.gated_mlp_backward(X, X, gate, up, down, saved)[0],
+             lambda: rl.gated_mlp(X, gate, up, down, mode_down=rl.MODE_SPARSE),
+             lambda: rl.rope(q, None, positions, plan)[0]]
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    for call, ref in zip(calls, want):
+        got, = in_threads([call])
+        assert isinstance(got, torch.Tensor), got
+        assert torch.equal(got, ref)
