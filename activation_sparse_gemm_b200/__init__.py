@@ -479,13 +479,16 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, w_q, w_k, positions, rope, eps=1
                                                     len(rope.axes), eps, out, weight_grads)
 
 
-def gated_mlp(X, W_gate, W_up, W_down, act=ACT_SILU, L_A=None, L_B=None, mode_down=MODE_DENSE_SKIP, save=False,
-              out=None, stream=None):
+def gated_mlp(X, W_gate, W_up, W_down, act=ACT_SILU, L_A=None, L_B=None, mode_down=None, save=False, out=None,
+              stream=None):
     """Y [M, D] of the gated feed-forward block, for contiguous bf16 CUDA tensors X [M, D], W_gate and W_up [D_ff, D],
     W_down [D, D_ff].
 
-    With mode_down=MODE_SPARSE the down-projection is the activation-sparse layer with the LoRA pair L_A [D, R],
-    L_B [R, D_ff].  With save=True the result is (Y, saved), saved = (G, U, low, H) for gated_mlp_backward
+    mode_down  None or MODE_DENSE_SKIP: Y = H W_down^T.  MODE_SPARSE: the activation-sparse layer, with the LoRA pair
+               L_A [D, R], L_B [R, D_ff] where both are given (MODE_DENSE_SKIP leaves a pair out, as linear() does;
+               None refuses one).
+
+    With save=True the result is (Y, saved), saved = (G, U, low, H) for gated_mlp_backward
     (low: the bits of G and U below bf16's, as int16; see include/rtlynx.h)."""
     with _HERE if stream is None else _on(X, stream):
         return _torch_calls().gated_mlp(X, W_gate, W_up, W_down, act, L_A, L_B, mode_down, save, out)

@@ -256,13 +256,22 @@ struct Gated {
     }
 };
 
+// mode: none given is the dense down-projection, where a LoRA pair would be
+// left out without a word; asked for by name, the dense one leaves it out as
+// the linear layer's does.
 py::object gated_mlp(const Tensor& X, const Tensor& W_gate, const Tensor& W_up, const Tensor& W_down, int act,
-                     const MaybeTensor& L_A, const MaybeTensor& L_B, int mode_down, bool save, const MaybeTensor& out) {
+                     const MaybeTensor& L_A, const MaybeTensor& L_B, const std::optional<int>& mode, bool save,
+                     const MaybeTensor& out) {
+    if (!mode && (L_A || L_B)) refuse("L_A and L_B belong to mode_down=MODE_SPARSE, no mode_down given");
+    const int mode_down = mode.value_or(RTLYNX_MODE_DENSE_SKIP);
+    const bool lora = mode_down != RTLYNX_MODE_DENSE_SKIP && (L_A || L_B);
+    if (lora && !(L_A && L_B)) refuse("one of L_A and L_B without the other");
+    if (lora && L_B->dim() != 2) refuse("L_B: a matrix [R, D_ff], got ", seen(*L_B));
     const Gated g(X, W_gate, W_up, W_down);
     const c10::cuda::CUDAGuard guard(X.device());
-    const int64_t R = L_A && L_B && mode_down != RTLYNX_MODE_DENSE_SKIP && L_B->dim() == 2 ? L_B->size(0) : 0;
-    const void* la = R ? matrix(*L_A, g.D, R, X, "L_A") : nullptr;
-    const void* lb = R ? matrix(*L_B, R, g.F, X, "L_B") : nullptr;
+    const int64_t R = lora ? L_B->size(0) : 0;
+    const void* la = lora ? matrix(*L_A, g.D, R, X, "L_A") : nullptr;
+    const void* lb = lora ? matrix(*L_B, R, g.F, X, "L_B") : nullptr;
     const Tensor Y = out ? *out : at::empty_like(X);
     void* y = matrix(Y, g.M, g.D, X, "out");
     const Tensor H = at::empty({g.M, g.F}, X.options());

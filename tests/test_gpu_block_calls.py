@@ -112,3 +112,21 @@ def test_first_call_of_a_host_thread(M, D, F):
         got, = in_threads([call])
         assert isinstance(got, torch.Tensor), got
         assert torch.equal(got, ref)
+
+
+def test_lora_pair_of_the_sparse_down_projection():
+    """Taken where the sparse form is asked for, left out where the dense one is, and refused in any other shape."""
+    M, D, F, R = 40, 264, 520, 16
+    (X, *W), call = sparse_call(M, D, F, R)
+    plain = rl.gated_mlp(X, *W, mode_down=rl.MODE_SPARSE)
+    assert not torch.equal(call(), plain)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    A, B = normal(gen, D, R), normal(gen, R, F)
+    assert torch.equal(rl.gated_mlp(X, *W, mode_down=rl.MODE_DENSE_SKIP, L_A=A, L_B=B), rl.gated_mlp(X, *W))
+    assert torch.equal(rl.gated_mlp(X, *W, mode_down=rl.MODE_SPARSE, L_A=A[:, :0], L_B=B[:0]), plain)
+    for la, lb in ((A, None), (None, B), (A, B.flatten()), (A[:, :8], B), (A, B[:8]), (A.T, B), (A, B.T), (A.float(), B),
+                   (A, B.cpu()), (A, B[:0])):
+        with pytest.raises(ValueError):
+            rl.gated_mlp(X, *W, mode_down=rl.MODE_SPARSE, L_A=la, L_B=lb)
+    with pytest.raises(ValueError):
+        rl.gated_mlp(X, *W, L_A=A, L_B=B)
