@@ -1,5 +1,5 @@
 """Builds the CUDA library librtlynx.so in-tree for sm_100a (nvcc, no GPU needed),
-and rtlynx_torch.so, the host code of its torch-level calls.
+and, where torch is installed, the host code of its torch-level calls (g++).
 
     python -m activation_sparse_gemm_b200.build [--force] [--verbose-ptxas]
 """
@@ -53,28 +53,43 @@ def needs_build() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
-def build_torch_calls(force: bool = False) -> str:
-    """Compiles the torch-level calls against the installed torch (g++, about 20 s)."""
-    if not force and os.path.exists(TORCH_LIB) and \
-            os.path.getmtime(TORCH_LIB) >= max(os.path.getmtime(TORCH_SRC), os.path.getmtime(HEADER)):
-        return TORCH_LIB
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+def torch_dir():
+    """Where torch is installed, or None."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
+
+
+def build_torch_calls(force: bool = False):
+    """Compiles the torch-level calls against the installed torch (g++, about 20 s); None where there is no torch."""
+    at = torch_dir()
+    if at is None:
+        return None
+    out = TORCH_LIB
+    if not force and os.path.exists(out) and \
+            os.path.getmtime(out) >= max(os.path.getmtime(TORCH_SRC), os.path.getmtime(HEADER)):
+        return out
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     os.makedirs(LIB_DIR, exist_ok=True)
-    tmp = TORCH_LIB + f".{os.getpid()}.tmp"
+    tmp = out + f".{os.getpid()}.tmp"
     subprocess.check_call([
         host_compiler(), "-O2", "-std=c++17", "-fPIC", "-shared",
         "-DTORCH_EXTENSION_NAME=rtlynx_torch", "-I" + sysconfig.get_paths()["include"],
-        "-I" + os.path.join(torch_dir, "include"),
-        "-I" + os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
-        "-I" + os.path.join(cuda, "include"), TORCH_SRC, "-o", tmp, "-L" + os.path.join(torch_dir, "lib"), "-lc10",
+        "-I" + os.path.join(at, "include"),
+        "-I" + os.path.join(at, "include", "torch", "csrc", "api", "include"),
+        "-I" + os.path.join(cuda, "include"), TORCH_SRC, "-o", tmp, "-L" + os.path.join(at, "lib"), "-lc10",
         "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"])
-    os.replace(tmp, TORCH_LIB)
-    return TORCH_LIB
+    os.replace(tmp, out)
+    return out
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    build_torch_calls(force)
+    build_library(force, verbose_ptxas)
+    if build_torch_calls(force) is None:
+        print("torch is not installed: librtlynx.so alone, without the torch-level calls", file=sys.stderr)
+    return LIB
+
+
+def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and not needs_build():
         return LIB
     os.makedirs(LIB_DIR, exist_ok=True)
