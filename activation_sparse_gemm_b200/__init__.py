@@ -23,10 +23,10 @@ import contextlib
 import ctypes
 import importlib.util
 import os
+import sysconfig
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "librtlynx.so")
-TORCH_LIB_PATH = os.path.join(_PKG, "_lib", "rtlynx_torch.so")
 
 MODE_SPARSE = 0
 MODE_DENSE_SKIP = 1
@@ -90,6 +90,11 @@ class RopeSpec(ctypes.Structure):
     _fields_ = [("n_axes", ctypes.c_int32), ("axis_dim", ctypes.c_int32 * MAX_AXES), ("pairing", ctypes.c_int32),
                 ("pos_type", ctypes.c_int32), ("theta", ctypes.c_double),
                 ("inv_freq", ctypes.POINTER(ctypes.c_double))]
+
+
+def torch_lib_path(torch_version: str) -> str:
+    """The host code of the torch-level calls, one file for each torch and Python that it was compiled against."""
+    return os.path.join(_PKG, "_lib", f"rtlynx_torch-{torch_version}-{sysconfig.get_config_var('SOABI')}.so")
 
 
 def lib() -> ctypes.CDLL:
@@ -388,11 +393,11 @@ _HERE = contextlib.nullcontext()
 def _torch_calls():
     global _calls
     if _calls is None:
-        import torch  # noqa: F401  (the extension needs its libraries in the process)
-        if not os.path.exists(TORCH_LIB_PATH):
-            raise RuntimeError(f"{TORCH_LIB_PATH} is missing: build it with "
-                               "`python -m activation_sparse_gemm_b200.build`")
-        spec = importlib.util.spec_from_file_location("rtlynx_torch", TORCH_LIB_PATH)
+        import torch  # the extension needs its libraries in the process
+        path = torch_lib_path(torch.__version__)
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m activation_sparse_gemm_b200.build`")
+        spec = importlib.util.spec_from_file_location("rtlynx_torch", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         L = lib()

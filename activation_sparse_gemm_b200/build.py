@@ -9,10 +9,13 @@ import argparse
 import glob
 import importlib.util
 import os
+import runpy
 import shutil
 import subprocess
 import sys
 import sysconfig
+
+from . import torch_lib_path
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,7 +23,6 @@ CSRC = os.path.join(PKG, "csrc")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "librtlynx.so")
 TORCH_SRC = os.path.join(CSRC, "torch_calls.cpp")
-TORCH_LIB = os.path.join(LIB_DIR, "rtlynx_torch.so")
 HEADER = os.path.join(ROOT, "include", "rtlynx.h")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -64,7 +66,7 @@ def build_torch_calls(force: bool = False):
     at = torch_dir()
     if at is None:
         return None
-    out = TORCH_LIB
+    out = torch_lib_path(runpy.run_path(os.path.join(at, "version.py"))["__version__"])
     if not force and os.path.exists(out) and \
             os.path.getmtime(out) >= max(os.path.getmtime(TORCH_SRC), os.path.getmtime(HEADER)):
         return out
