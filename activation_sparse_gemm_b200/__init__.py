@@ -445,13 +445,25 @@ class Rope:
             values = [float(v) for v in inv_freq]
             if len(values) != pairs:
                 raise ValueError(f"inv_freq has {len(values)} values, the axes {pairs} pairs")
+        self._lay_out(int(pairing), values)
+
+    def _lay_out(self, pairing, values):
         # the calls read the frequencies from here, so no call has to raise theta to 64 powers
-        self._freq = (ctypes.c_double * pairs)(*values)
+        self._freq = (ctypes.c_double * len(values))(*values)
         dims = (ctypes.c_int32 * MAX_AXES)(*self.axes)
         freq = ctypes.cast(self._freq, ctypes.POINTER(ctypes.c_double))
-        self.specs = (RopeSpec * 3)(*(RopeSpec(len(self.axes), dims, int(pairing), t, 0.0, freq)
+        self.specs = (RopeSpec * 3)(*(RopeSpec(len(self.axes), dims, pairing, t, 0.0, freq)
                                       for t in (POS_INT32, POS_INT64, POS_FP32)))
         self._at = ctypes.addressof(self.specs)
+
+    # A copy, or what another process unpickles, has a layout of its own: addresses do not travel.
+    def __getstate__(self):
+        state = {name: value for name, value in self.__dict__.items() if name not in ("_freq", "specs", "_at")}
+        return state, self.specs[0].pairing, list(self._freq)
+
+    def __setstate__(self, state):
+        self.__dict__.update(state[0])
+        self._lay_out(*state[1:])
 
 
 def rope(q, k, positions, rope, out=None, stream=None):
