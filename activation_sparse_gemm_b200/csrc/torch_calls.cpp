@@ -10,8 +10,11 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
 
+#include <array>
 #include <optional>
 #include <sstream>
+#include <tuple>
+#include <variant>
 
 #include "../../include/rtlynx.h"
 
@@ -177,7 +180,7 @@ Pair outputs(const MaybePair& out, const Tensor& q, const MaybeTensor& k) {
     return inputs(qo, ko, q, nullptr, nullptr, "q_out", "k_out");
 }
 
-py::tuple rope(bool backward, const Tensor& q, const MaybeTensor& k, const Tensor& positions, uintptr_t specs, int64_t axes,
+std::tuple<Tensor, MaybeTensor> rope(bool backward, const Tensor& q, const MaybeTensor& k, const Tensor& positions, uintptr_t specs, int64_t axes,
                const MaybePair& out) {
     const Heads h(q);
     const c10::cuda::CUDAGuard guard(q.device());
@@ -188,10 +191,10 @@ py::tuple rope(bool backward, const Tensor& q, const MaybeTensor& k, const Tenso
                                                     p.data, p.b, p.s, p.a,
                                                     c10::cuda::getCurrentCUDAStream(q.get_device()).stream()),
           backward ? "rtlynx_rope_backward" : "rtlynx_rope");
-    return py::make_tuple(o.q, o.k);
+    return {o.q, o.k};
 }
 
-py::tuple qk_norm_rope(const Tensor& q, const MaybeTensor& k, const MaybeTensor& w_q, const MaybeTensor& w_k,
+std::tuple<Tensor, MaybeTensor> qk_norm_rope(const Tensor& q, const MaybeTensor& k, const MaybeTensor& w_q, const MaybeTensor& w_k,
                        const Tensor& positions, uintptr_t specs, int64_t axes, double eps, const MaybePair& out) {
     const Heads h(q);
     const c10::cuda::CUDAGuard guard(q.device());
@@ -202,10 +205,11 @@ py::tuple qk_norm_rope(const Tensor& q, const MaybeTensor& k, const MaybeTensor&
     check(api.norm_rope(&in.qv, in.keys(), wq, wk, &o.qv, o.keys(), h.B, h.S, h.D, h.dtype, static_cast<float>(eps), p.spec,
                         p.data, p.b, p.s, p.a, c10::cuda::getCurrentCUDAStream(q.get_device()).stream()),
           "rtlynx_qk_norm_rope");
-    return py::make_tuple(o.q, o.k);
+    return {o.q, o.k};
 }
 
-py::tuple qk_norm_rope_backward(const Tensor& dq_out, const MaybeTensor& dk_out, const Tensor& q, const MaybeTensor& k,
+using HeadGrads = std::tuple<Tensor, MaybeTensor, MaybeTensor, MaybeTensor>;
+HeadGrads qk_norm_rope_backward(const Tensor& dq_out, const MaybeTensor& dk_out, const Tensor& q, const MaybeTensor& k,
                                 const MaybeTensor& w_q, const MaybeTensor& w_k, const Tensor& positions, uintptr_t specs,
                                 int64_t axes, double eps, const MaybePair& out, bool weight_grads) {
     const Heads h(q);
@@ -229,7 +233,7 @@ py::tuple qk_norm_rope_backward(const Tensor& dq_out, const MaybeTensor& dk_out,
                                  static_cast<float>(eps), p.spec, p.data, p.b, p.s, p.a, data(ws), n,
                                  c10::cuda::getCurrentCUDAStream(q.get_device()).stream()),
           "rtlynx_qk_norm_rope_backward");
-    return py::make_tuple(o.q, o.k, dw_q, dw_k);
+    return {o.q, o.k, dw_q, dw_k};
 }
 
 // ---------------------------------------------------------------- gated feed-forward block
@@ -259,7 +263,8 @@ struct Gated {
 // mode: none given is the dense down-projection, where a LoRA pair would be
 // left out without a word; asked for by name, the dense one leaves it out as
 // the linear layer's does.
-py::object gated_mlp(const Tensor& X, const Tensor& W_gate, const Tensor& W_up, const Tensor& W_down, int act,
+using Saved = std::tuple<Tensor, Tensor, Tensor, Tensor>;
+std::variant<Tensor, std::tuple<Tensor, Saved>> gated_mlp(const Tensor& X, const Tensor& W_gate, const Tensor& W_up, const Tensor& W_down, int act,
                      const MaybeTensor& L_A, const MaybeTensor& L_B, const std::optional<int>& mode, bool save,
                      const MaybeTensor& out) {
     if (!mode && (L_A || L_B)) refuse("L_A and L_B belong to mode_down=MODE_SPARSE, no mode_down given");
@@ -287,13 +292,13 @@ py::object gated_mlp(const Tensor& X, const Tensor& W_gate, const Tensor& W_up, 
     check(api.gated(g.x, g.gate, g.up, g.down, la, lb, data(G), data(U), data(low), H.data_ptr(), y, g.M, g.D, g.F, R, act,
                     mode_down, data(ws), n, c10::cuda::getCurrentCUDAStream(X.get_device()).stream()),
           "rtlynx_gated_mlp_block");
-    if (!save) return py::cast(Y);
-    return py::make_tuple(Y, py::make_tuple(*G, *U, *low, H));
+    if (!save) return Y;
+    return std::tuple<Tensor, Saved>(Y, Saved(*G, *U, *low, H));
 }
 
-py::tuple gated_mlp_backward(const Tensor& dY, const Tensor& X, const Tensor& W_gate, const Tensor& W_up,
-                             const Tensor& W_down, const std::tuple<Tensor, Tensor, Tensor, Tensor>& saved, int act,
-                             const std::array<bool, 4>& needs) {
+using GatedGrads = std::tuple<MaybeTensor, MaybeTensor, MaybeTensor, MaybeTensor>;
+GatedGrads gated_mlp_backward(const Tensor& dY, const Tensor& X, const Tensor& W_gate, const Tensor& W_up,
+                              const Tensor& W_down, const Saved& saved, int act, const std::array<bool, 4>& needs) {
     const Gated g(X, W_gate, W_up, W_down);
     const c10::cuda::CUDAGuard guard(X.device());
     const void* dy = matrix(dY, g.M, g.D, X, "dY");
@@ -310,7 +315,7 @@ py::tuple gated_mlp_backward(const Tensor& dY, const Tensor& X, const Tensor& W_
     check(api.gated_backward(dy, g.x, g.gate, g.up, g.down, G, U, low, H, data(d[0]), data(d[1]), data(d[2]), data(d[3]), g.M,
                              g.D, g.F, act, ws.data_ptr(), n, c10::cuda::getCurrentCUDAStream(X.get_device()).stream()),
           "rtlynx_gated_mlp_backward");
-    return py::make_tuple(d[0], d[1], d[2], d[3]);
+    return {d[0], d[1], d[2], d[3]};
 }
 
 }  // namespace
@@ -325,9 +330,12 @@ PYBIND11_MODULE(rtlynx_torch, m) {
         }
     });
     m.def("bind", &bind);
-    m.def("rope", &rope);
-    m.def("qk_norm_rope", &qk_norm_rope);
-    m.def("qk_norm_rope_backward", &qk_norm_rope_backward);
-    m.def("gated_mlp", &gated_mlp);
-    m.def("gated_mlp_backward", &gated_mlp_backward);
+    // Without Python's lock from the arguments' conversion to the results': a
+    // launch waits where the stream's queue is full, and torch's allocator may.
+    using Unlocked = py::call_guard<py::gil_scoped_release>;
+    m.def("rope", &rope, Unlocked());
+    m.def("qk_norm_rope", &qk_norm_rope, Unlocked());
+    m.def("qk_norm_rope_backward", &qk_norm_rope_backward, Unlocked());
+    m.def("gated_mlp", &gated_mlp, Unlocked());
+    m.def("gated_mlp_backward", &gated_mlp_backward, Unlocked());
 }

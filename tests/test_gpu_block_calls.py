@@ -1,5 +1,6 @@
 """Calls of the query/key and gated operators as programs make them: handles of streams, several host threads."""
 import threading
+import time
 
 import pytest
 import torch
@@ -130,3 +131,60 @@ def test_lora_pair_of_the_sparse_down_projection():
             rl.gated_mlp(X, *W, mode_down=rl.MODE_SPARSE, L_A=la, L_B=lb)
     with pytest.raises(ValueError):
         rl.gated_mlp(X, *W, L_A=A, L_B=B)
+
+
+@pytest.mark.parametrize("which", ["rope", "gated_mlp"])
+def test_other_host_threads_run_while_a_launch_waits(which):
+    """More launches than a stream's queue holds, behind a kernel of about a second: one of them waits for it, and this
+    thread meanwhile goes on.  Held up, it would stand still as long as that call."""
+    X, *W = gated_inputs(2, 64, 128)
+    out = torch.empty_like(X)
+    positions, plan = torch.zeros(2, 1, dtype=torch.int32, device="cuda"), rl.Rope((64,))
+    q, q_out = X.view(2, 1, 64), out.view(2, 1, 64)
+    calls = {"rope": lambda: rl.rope(q, None, positions, plan, out=(q_out, None)),
+             "gated_mlp": lambda: rl.gated_mlp(X, *W, out=out)}
+    call = calls[which]
+    call()
+    torch.cuda.synchronize()
+    waited = 0.0
+
+    def work():
+        nonlocal waited
+        torch.cuda._sleep(2_000_000_000)
+        for _ in range(4000):
+            before = time.perf_counter()
+            call()
+            waited = max(waited, time.perf_counter() - before)
+
+    thread = threading.Thread(target=work)
+    thread.start()
+    stood, last = 0.0, time.perf_counter()
+    while thread.is_alive():
+        time.sleep(0.002)
+        now = time.perf_counter()
+        stood, last = max(stood, now - last), now
+    torch.cuda.synchronize()
+    assert waited > 0.2, "nothing waited: the queue is longer than this test takes it to be"
+    assert stood < waited / 2
+
+
+@pytest.mark.parametrize("mode", [rl.MODE_DENSE_SKIP, rl.MODE_SPARSE])
+def test_host_threads_on_one_stream(mode):
+    """Each of several threads gets its own results, whatever the others launch between its kernels."""
+    stream = torch.cuda.Stream()
+    jobs = []
+    for i, (M, D, F) in enumerate(SPARSE):
+        args = gated_inputs(M, D, F, seed=i)
+        jobs.append((args, rl.gated_mlp(*args, mode_down=mode)))
+    torch.cuda.synchronize()
+
+    def work(args, want):
+        for _ in range(40):
+            got = [rl.gated_mlp(*args, mode_down=mode, stream=stream) for _ in range(5)]
+            stream.synchronize()
+            if not all(torch.equal(y, want) for y in got):
+                return "wrong"
+        return "right"
+
+    assert in_threads([lambda job=job: work(*job) for job in jobs]) == ["right"] * len(jobs)
+    assert rl.rtlynx_stream_status() == rl.OK
