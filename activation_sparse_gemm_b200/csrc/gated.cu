@@ -686,17 +686,18 @@ int launch_tiles(const GatedArgs& args, int num_sms, cudaStream_t stream) {
 }
 
 // The tiled kernel; where anything was split, the plain one, whose units
-// leave partial tiles, and the sums with the epilogue asked for.
+// leave partial tiles, and the sums with the epilogue asked for.  (The gate and
+// up projections are never split: launch_tiles.)
 template <int EPI, int ACT, int TN = kTile>
 int launch_gated(const GatedArgs& args, int num_sms, cudaStream_t stream) {
+    static_assert(EPI != kGatedForward, "has no sums of its own");
     int tiles = 0;
     for (int i = 0; i < args.problems; ++i)
         if (args.p[i].split > 1 && args.p[i].m_pairs * args.p[i].n_tiles > tiles) tiles = args.p[i].m_pairs * args.p[i].n_tiles;
-    if (EPI == kGatedForward || tiles == 0) return launch_tiles<EPI, ACT, TN>(args, num_sms, stream);
+    if (tiles == 0) return launch_tiles<EPI, ACT, TN>(args, num_sms, stream);
     const int e = launch_tiles<kStore, 0, kTile>(args, num_sms, stream);
     if (e) return e;
-    constexpr int kSum = EPI == kGatedForward ? kStore : EPI;
-    return launch_dependent(rtlynx_gated_sum_parts_kernel<kSum, ACT>, dim3(2 * tiles, 16, args.problems), dim3(256), 0,
+    return launch_dependent(rtlynx_gated_sum_parts_kernel<EPI, ACT>, dim3(2 * tiles, 16, args.problems), dim3(256), 0,
                             stream, args);
 }
 
@@ -1009,11 +1010,11 @@ int rtlynx_gated_mlp_block(const void* X, const void* W_gate, const void* W_up, 
         args.units = p.m_pairs * p.n_tiles;
         int e;
         if (act == RTLYNX_ACT_SILU)
-            e = narrow ? launch_gated<kGatedForward, RTLYNX_ACT_SILU, kNarrow>(args, num_sms, stream)
-                       : launch_gated<kGatedForward, RTLYNX_ACT_SILU>(args, num_sms, stream);
+            e = narrow ? launch_tiles<kGatedForward, RTLYNX_ACT_SILU, kNarrow>(args, num_sms, stream)
+                       : launch_tiles<kGatedForward, RTLYNX_ACT_SILU, kTile>(args, num_sms, stream);
         else
-            e = narrow ? launch_gated<kGatedForward, RTLYNX_ACT_GELU, kNarrow>(args, num_sms, stream)
-                       : launch_gated<kGatedForward, RTLYNX_ACT_GELU>(args, num_sms, stream);
+            e = narrow ? launch_tiles<kGatedForward, RTLYNX_ACT_GELU, kNarrow>(args, num_sms, stream)
+                       : launch_tiles<kGatedForward, RTLYNX_ACT_GELU, kTile>(args, num_sms, stream);
         if (e) return RTLYNX_ERR_CUDA;
     }
     if (sparse)
