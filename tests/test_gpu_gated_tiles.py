@@ -143,3 +143,28 @@ def test_output_given():
     for bad in (X, W[2][:M].view(-1)[:M * D].view(M, D)):
         with pytest.raises(rl.RtlynxError):
             rl.gated_mlp(X, *W, out=bad)
+
+
+def test_hidden_arrays_beyond_32_bits():
+    """H, G, U, dG and dU of more than 2^31 elements: the rows past that point are what a call on them alone gives.
+    Whole numbers, so that both are exact whatever the kernel."""
+    M, D, F, part = 530000, 8, 4104, 300
+    assert (M - part) * F > 1 << 31
+    gen, X, Wg, Wu = whole_number_inputs(part, D, F, 5)
+    W = dev(Wg), dev(Wu), dev(ints(gen, (D, F), -1, 1, 0.5))
+    last, dY = dev(X), dev(ints(gen, (part, D), -1, 1, 0.25))
+    many = last.repeat(-(-M // part), 1)[:M].contiguous()
+    many[-part:] = last
+    far = torch.zeros_like(many)
+    far[-part:] = dY
+    want, kept = rl.gated_mlp(last, *W, save=True)
+    got, saved = rl.gated_mlp(many, *W, save=True)
+    assert torch.equal(got[-part:], want)
+    for a, b in zip(saved, kept):
+        assert torch.equal(a[-part:], b)
+    grads = rl.gated_mlp_backward(far, many, *W, saved)
+    ref = rl.gated_mlp_backward(dY, last, *W, kept)
+    assert torch.equal(grads[0][-part:], ref[0]) and not grads[0][:-part].any()
+    for a, b in zip(grads[1:], ref[1:]):
+        assert torch.equal(a, b)
+    assert rl.rtlynx_stream_status() == rl.OK
