@@ -385,7 +385,8 @@ def linear(X, W, L_A=None, L_B=None, mode: int = MODE_SPARSE, out=None, stream=N
 
 
 # The operators around the linear layers.  Checks, outputs and the call itself are compiled (csrc/torch_calls.cpp):
-# a call on a few tokens is as long as its host part.
+# a call on a few tokens is as long as its host part.  They record nothing for autograd: an output carries no history,
+# whatever its inputs require, and gradients come from the _backward calls.
 _calls = None
 _HERE = contextlib.nullcontext()
 

@@ -18,9 +18,9 @@
 // adds them in order.
 //
 // Measured, TFLOP/s of the call (the measured cuBLAS rate is 1632 in a burst and
-// 1354 under the power cap): forward at 32760 x 5120 -> 13824 1370-1570 by the
-// power state, training step on 8192 tokens 1270-1530.  Tensor pipe active
-// 85% (gate and up), 78% (down), 79% (dH) and 86% (gradients) at 4096 tokens.
+// 1354 under the power cap): forward at 32760 x 5120 -> 13824 1354-1590 by the
+// power state, training step on 8192 tokens 1266-1530.  Tensor pipe active
+// 92% (gate and up), 83% (down), 88% (dH) and 96% (gradients) at 4096 tokens.
 // A stage's operands are 32 KB a CTA for 512 cycles of MMAs, so L2 has to deliver
 // 64 bytes a cycle to every SM: rows that do not start on 128-byte lines (widths
 // not a multiple of 64) stretch a stage to about 700 cycles.  With D below about 512
@@ -899,7 +899,8 @@ struct BackwardLayout {
 
 // Values from one row of dG and dU to the next: they live in the workspace, so
 // their rows start on 128-byte lines whatever D_ff (2047 tokens at 1544 -> 4104:
-// training step 277 us with rows of D_ff values, 258 like this).
+// training step 276 us with rows of D_ff values, 257 like this, after pauses; 296
+// to 302 like this in a long run).
 int64_t hidden_pitch(int64_t F) { return (F + 63) / 64 * 64; }
 
 // The workspace does for any choice of gradients.

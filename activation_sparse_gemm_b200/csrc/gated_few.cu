@@ -24,7 +24,7 @@
 // Measured at D = 5120, D_ff = 13824 (424.7 MB of weights, 64.9 us at the
 // measured copy rate): 1 token 67 us (6.4 TB/s), 8 tokens 69; 16 tokens 88, as a
 // block re-reads the tokens from L2 half as often as it reads weights, which is
-// where gated_some.cu takes over.  11 tokens at 2056 -> 5512: 21 us.
+// where gated_some.cu takes over.  11 tokens at 2056 -> 5512: 20.8 us.
 #include "../../include/rtlynx.h"
 #include "act.cuh"
 #include "internal.h"
@@ -195,14 +195,15 @@ int launch_few(const FewArgs& args, cudaStream_t stream) {
     const dim3 grid((args.N + kFewRows - 1) / kFewRows, (args.M + 15) / 16);
     const int blocks = static_cast<int>(grid.x * grid.y);
     // Sixteen warps where there are no more blocks than SMs, so that enough
-    // loads are in flight: at 2056 -> 5512 and 11 tokens the call takes 19.3 us,
-    // 25.1 with eight.  With more blocks eight are as good or better (70 against
+    // loads are in flight: at 2056 -> 5512 and 11 tokens, where that is the
+    // down-projection, the call takes 20.8 us, 23.7 with eight.  With more blocks eight are as good or better (70 against
     // 77 us at 5120 -> 13824, one token).
     if (blocks <= num_sms) return launch_warps<GATED, ACT, 16, 1>(args, grid, stream);
     // Past eight tokens two blocks of 128 registers a thread on an SM, three of
     // 80 where they are all resident then (11 tokens at 1536 -> 4096: 12.0 us,
-    // 13.6 with three; at 2056 -> 5512 22.1 and 21.2).  Up to eight tokens three
-    // (one at 5120 -> 13824: 66.6 us, 75.4 with two).
+    // 13.6 with three; at 2056 -> 5512 22.1 and 21.2, although 80 registers spill 52
+    // bytes of the gated kernel).  Up to eight tokens three (one at 5120 -> 13824:
+    // 66.6 us, 75.4 with two).
     if (blocks > 2 * num_sms && blocks <= 3 * num_sms) return launch_warps<GATED, ACT, 8, 3>(args, grid, stream);
     return launch_warps<GATED, ACT, 8, 2>(args, grid, stream);
 }

@@ -22,8 +22,10 @@
 // (f32x2): the norm's gradient took 195 us without, 179 with.
 //
 // Measured (32760 tokens, 40 + 40 heads of 128, bf16, 1.34 GB): rotation 207 us
-// (6.5 TB/s, the measured copy rate), with the norm 220 us (6.1 TB/s); gradient
-// of both on 16384 tokens (1.01 GB) 160 us (6.3 TB/s).
+// (6.5 TB/s, the measured copy rate), with the norm 218 us (6.1 TB/s); gradient
+// of both on 16384 tokens (1.01 GB) 160 us (6.3 TB/s).  That is after pauses: in a
+// long run, which reaches the power cap (980 W, 1.7 GHz of 1.97), 209, 231 and
+// 181 us (the last 5.6 TB/s).
 //
 // Angles: position x frequency / 2 pi in 64 bits, reduced to an eighth of a
 // turn there, so a position of 2^24 loses nothing; sine and cosine of the
@@ -242,7 +244,8 @@ __global__ void __launch_bounds__(kHeadThreads, KIND == kNormBackward ? 2 : 4) r
     // loaded before these are computed.  Registers decide: forward, 64 of them
     // leave 32 warps an SM, which hide the latency without looking ahead
     // (video workload's norm: 229 us when measured; two heads and looking
-    // ahead 235, 80 registers 249); backward, with two tensors read and the weights' sums
+    // ahead 235, 80 registers 249), though the norm's instances spill 16 to 92
+    // bytes a thread for it (24 at 128 channels in 16 bits, 48 with half pairing); backward, with two tensors read and the weights' sums
     // kept, 128 and 16 warps, looking ahead (179 us when
     // measured; without 205, two heads 190).
     // Half pairing of a 16-bit type takes two loads for a lane's channels: two

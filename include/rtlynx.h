@@ -262,8 +262,9 @@ int rtlynx_gated_mlp_backward(const void* dY, const void* X, const void* W_gate,
  * turned, the rest pass through.  The pairs of axis a follow those of axis
  * a - 1; pair j of an axis of d channels has f = theta^(-2 j / d), or
  * inv_freq[i] where the caller gives frequencies of its own.
- * Angles are taken to one turn in 64 bits, so far positions lose nothing;
- * everything else is in 32, each output rounded once.
+ * Angles are taken to one turn in 64 bits (off by a few 2^-53 of the whole
+ * angle: nothing to an output at positions of 2^24); everything else is in 32,
+ * each output rounded once.
  */
 typedef enum { RTLYNX_BF16 = 0, RTLYNX_FP16 = 1, RTLYNX_FP32 = 2 } rtlynx_dtype;
 
